@@ -362,6 +362,57 @@ KVQ_API kvq_status kvq_paged_decode_attention_static_scratch(
     const void* k_tail, const void* v_tail, float softmax_scale, int num_splits, int32_t* dev_status,
     void* stream);
 
+/* Bytes of device workspace kvq_prompt_attention needs with masses on the
+ * current device (none without).  cfg, bytes: host pointers. */
+KVQ_API kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seqs, int total_tokens,
+                                              int max_seq_tokens, int mass_window, size_t* bytes);
+
+/* Read path, whole prompts: causal attention over raw fp16 rows, before (or
+ * beside) their quantization into an empty cache.  Token i of sequence s
+ * (query head j, reading KV head j / group_size) attends to tokens 0..i of
+ * its sequence: softmax(q.k * softmax_scale) V, statistics and sums in fp32,
+ * the weights rounded to fp16 for the product with V.
+ *   q            : device fp16, total_tokens rows of [num_kv_heads*group_size][d],
+ *                  q_stride elements from row to row; not rotated.
+ *   k, v         : device fp16, total_tokens rows of [num_kv_heads][d], k_stride
+ *                  and v_stride elements from row to row.  Strides are multiples
+ *                  of 8 and at least a row, so that q, k and v may be slices of
+ *                  one projection's output.
+ *   out          : device fp16 [total_tokens][num_kv_heads*group_size][d].
+ *   lse          : device fp32 [total_tokens][num_kv_heads*group_size], the
+ *                  natural log of the row's sum of exp(q.k * softmax_scale); may
+ *                  be NULL.
+ *   cu_seqlens   : device int32 [num_seqs+1], prefix sums of the sequence
+ *                  lengths: sequence s is rows cu_seqlens[s] .. cu_seqlens[s+1]-1.
+ *                  Rows in no sequence are not read into any result and their
+ *                  out and lse are left as they were.
+ *   max_seq_tokens: host bound >= every length, at most 2^20.
+ *   mass         : device fp32 [num_seqs][max_tiles] or NULL.  Entry (s, t) grows
+ *                  by the attention weight that the tokens of tile t
+ *                  (tile_tokens tokens from t * tile_tokens on) of sequence s
+ *                  receive from the queries that count, summed over query heads
+ *                  (every counting row adds 1 to its sequence in all); the same
+ *                  tiles as the cache's after the prompt is quantized.  max_tiles
+ *                  x tile_tokens must hold max_seq_tokens.  The sums do not
+ *                  depend on the launch: two calls give the same bits.
+ *   mass_window  : the queries that count are the last mass_window tokens of
+ *                  each sequence; 0: all.  0 without mass.
+ *   workspace    : device, >= kvq_prompt_workspace_bytes(...) bytes, with mass
+ *                  only (else NULL); contents on entry are ignored.  Calls that
+ *                  overlap in time need one each.
+ * A row that sees a NaN, or an infinite score, gives NaN; values that a row
+ * does not see (later tokens, other sequences, rows behind the last one) never
+ * reach it, whatever they are.  A sequence whose prefix sums are negative,
+ * descending, past total_tokens or longer than max_seq_tokens is skipped and
+ * reported through dev_status (KVQ_ERR_DEVICE_BOUNDS).  All pointers 16-byte
+ * aligned; the call is asynchronous on stream. */
+KVQ_API kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int q_stride, const void* k,
+                                        int k_stride, const void* v, int v_stride, void* out, float* lse,
+                                        const int32_t* cu_seqlens, int num_seqs, int total_tokens,
+                                        int max_seq_tokens, float softmax_scale, float* mass, int max_tiles,
+                                        int mass_window, void* workspace, size_t workspace_bytes,
+                                        int32_t* dev_status, void* stream);
+
 /* Inspection (tests, tools): read num_tiles tiles back out of a pool.
  *   tile_desc : device int32 [num_tiles][2] = {seq, tile_idx}; all heads.
  *   is_v      : 0 = K pool / bits_k, 1 = V pool / bits_v.

@@ -81,6 +81,23 @@ kvq_status check_tables(const int32_t* block_tables, int max_blocks_per_seq, int
   return KVQ_OK;
 }
 
+kvq_status check_prompt_sizes(const kvq_config* cfg, int num_seqs, int total_tokens, int max_seq_tokens,
+                              int mass_window) {
+  if (num_seqs < 0 || total_tokens < 0 || max_seq_tokens < 0 || mass_window < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs, total_tokens, max_seq_tokens or mass_window");
+  if (num_seqs > 65535) return fail(KVQ_ERR_INVALID_ARG, "num_seqs > 65535");
+  if (max_seq_tokens > (1 << 20)) return fail(KVQ_ERR_INVALID_ARG, "max_seq_tokens > 2^20");
+  if (kvq::prompt_units(*cfg, num_seqs, total_tokens) > 0x3fffffffLL)
+    return fail(KVQ_ERR_INVALID_ARG, "num_seqs x total_tokens x num_kv_heads too large for one launch");
+  return KVQ_OK;
+}
+
+kvq_status check_row_stride(int stride, int row, const char* name) {
+  if (stride < row) return fail(KVQ_ERR_INVALID_ARG, "%s %d is less than a row of %d elements", name, stride, row);
+  if (stride % 8 != 0) return fail(KVQ_ERR_INVALID_ARG, "%s must be a multiple of 8 elements (got %d)", name, stride);
+  return KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -408,6 +425,75 @@ kvq_status kvq_paged_prefill_attention(const kvq_config* cfg, const void* q, voi
                        "kvq_paged_prefill_attention launch");
   return cuda_status(kvq::launch_paged_prefill(a, static_cast<cudaStream_t>(stream)),
                      "kvq_paged_prefill_attention launch");
+}
+
+kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seqs, int total_tokens, int max_seq_tokens,
+                                      int mass_window, size_t* bytes) {
+  KVQ_TRY(check_config(cfg));
+  if (bytes == nullptr) return fail(KVQ_ERR_INVALID_ARG, "bytes output is NULL");
+  KVQ_TRY(check_prompt_sizes(cfg, num_seqs, total_tokens, max_seq_tokens, mass_window));
+  int sms = 0;
+  KVQ_TRY(device_sm_count(&sms));
+  *bytes = kvq::prompt_workspace_bytes(*cfg, num_seqs, total_tokens, max_seq_tokens, mass_window, sms);
+  return ok();
+}
+
+kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int q_stride, const void* k, int k_stride,
+                                const void* v, int v_stride, void* out, float* lse, const int32_t* cu_seqlens,
+                                int num_seqs, int total_tokens, int max_seq_tokens, float softmax_scale, float* mass,
+                                int max_tiles, int mass_window, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream) {
+  KVQ_TRY(check_config(cfg));
+  KVQ_TRY(check_prompt_sizes(cfg, num_seqs, total_tokens, max_seq_tokens, mass_window));
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 1e30f))
+    return fail(KVQ_ERR_INVALID_ARG, "softmax_scale must be a positive finite float");
+  const int row_q = cfg->num_kv_heads * cfg->group_size * cfg->head_dim, row_kv = cfg->num_kv_heads * cfg->head_dim;
+  KVQ_TRY(check_row_stride(q_stride, row_q, "q_stride"));
+  KVQ_TRY(check_row_stride(k_stride, row_kv, "k_stride"));
+  KVQ_TRY(check_row_stride(v_stride, row_kv, "v_stride"));
+  if (mass == nullptr && mass_window != 0) return fail(KVQ_ERR_INVALID_ARG, "mass_window without mass");
+  if (mass != nullptr && static_cast<long long>(max_tiles) * cfg->tile_tokens < max_seq_tokens)
+    return fail(KVQ_ERR_INVALID_ARG, "max_tiles %d x %d tokens holds no sequence of %d", max_tiles, cfg->tile_tokens,
+                max_seq_tokens);
+  if (num_seqs == 0 || total_tokens == 0 || max_seq_tokens == 0) return ok();
+  KVQ_TRY(check_ptr(q, "q"));
+  KVQ_TRY(check_ptr(k, "k"));
+  KVQ_TRY(check_ptr(v, "v"));
+  KVQ_TRY(check_ptr(out, "out"));
+  KVQ_TRY(check_ptr(lse, "lse", true));
+  KVQ_TRY(check_ptr(cu_seqlens, "cu_seqlens"));
+  KVQ_TRY(check_ptr(mass, "mass", true));
+  KVQ_TRY(check_ptr(workspace, "workspace", mass == nullptr));
+  KVQ_TRY(check_ptr(dev_status, "dev_status", true));
+  if (mass != nullptr) {
+    int sms = 0;
+    KVQ_TRY(device_sm_count(&sms));
+    const size_t need = kvq::prompt_workspace_bytes(*cfg, num_seqs, total_tokens, max_seq_tokens, mass_window, sms);
+    if (workspace_bytes < need)
+      return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  }
+  kvq::PromptArgs a{};
+  a.cfg = *cfg;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.out = out;
+  a.lse = lse;
+  a.cu_seqlens = cu_seqlens;
+  a.num_seqs = num_seqs;
+  a.total_tokens = total_tokens;
+  a.max_seq_tokens = max_seq_tokens;
+  a.softmax_scale = softmax_scale;
+  a.mass = mass;
+  a.max_tiles = max_tiles;
+  a.mass_window = mass_window;
+  a.workspace = workspace;
+  a.dev_status = dev_status;
+  return cuda_status(kvq::launch_prompt_attention(a, static_cast<cudaStream_t>(stream)),
+                     "kvq_prompt_attention launch");
 }
 
 kvq_status kvq_unpack_tiles(const kvq_config* cfg, const int32_t* tile_desc, int num_tiles,

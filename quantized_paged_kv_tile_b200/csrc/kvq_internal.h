@@ -149,6 +149,32 @@ int prefill_row_tiles(const kvq_config& cfg, int max_chunk);
 size_t prefill_workspace_bytes(const kvq_config& cfg, int num_seqs, int max_chunk, int num_splits);
 cudaError_t launch_paged_prefill(const PrefillArgs& a, cudaStream_t s);
 
+struct PromptArgs {
+  kvq_config cfg;
+  const void* q;              // [total_tokens] rows of [H_kv*g][d] fp16, q_stride elements apart
+  const void* k;              // [total_tokens] rows of [H_kv][d] fp16
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  void* out;                  // [total_tokens][H_kv*g][d] fp16
+  float* lse;                 // [total_tokens][H_kv*g], may be null
+  const int32_t* cu_seqlens;  // [B+1]
+  int num_seqs;
+  int total_tokens;           // rows of q, k, v
+  int max_seq_tokens;         // host bound on sequence lengths
+  float softmax_scale;
+  float* mass;                // [B][max_tiles], added to; null: no masses
+  int max_tiles;
+  int mass_window;            // queries that count: the last mass_window of a sequence; 0: all
+  void* workspace;
+  int32_t* dev_status;
+};
+// work units of a call (host bound)
+long long prompt_units(const kvq_config& cfg, int num_seqs, int total_tokens);
+// workspace of a call with masses on a device with `sms` SMs
+size_t prompt_workspace_bytes(const kvq_config& cfg, int num_seqs, int total_tokens, int max_seq_tokens, int window,
+                              int sms);
+cudaError_t launch_prompt_attention(const PromptArgs& a, cudaStream_t s);
+
 // Head sizes 64 and 256 (kvq_generic.cu): the same calls on the CUDA cores;
 // the launchers above hand configurations with head_dim != 128 to these.
 cudaError_t launch_generic_quantize(const QuantizeArgs& a, cudaStream_t s);

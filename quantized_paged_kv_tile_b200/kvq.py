@@ -31,6 +31,7 @@ EXPORTED_SYMBOLS = (
     "kvq_paged_decode_attention", "kvq_paged_decode_attention_static_scratch", "kvq_unpack_tiles",
     "kvq_selftest_bounded_wait", "kvq_status_string", "kvq_last_error", "kvq_version",
     "kvq_prefill_workspace_bytes", "kvq_paged_prefill_attention", "kvq_append_decode_step",
+    "kvq_prompt_workspace_bytes", "kvq_prompt_attention",
 )
 
 
@@ -102,6 +103,9 @@ _SIGNATURES = {
     "kvq_prefill_workspace_bytes": [_cfgp, _i32, _i32, _i32, ctypes.POINTER(_sz)],
     "kvq_paged_prefill_attention": [_cfgp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp,
                                     _vp, _vp, _f32, _i32, _vp, _sz, _vp, _vp],
+    "kvq_prompt_workspace_bytes": [_cfgp, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)],
+    "kvq_prompt_attention": [_cfgp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp,
+                             _i32, _i32, _vp, _sz, _vp, _vp],
     "kvq_unpack_tiles": [_cfgp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
 }
 
@@ -314,6 +318,56 @@ def paged_prefill_attention(cfg: Config, q, out, k_new, v_new, cu_chunk, ctx_len
         int(num_splits), _ptr(workspace, "workspace", torch.uint8), 0 if workspace is None else workspace.numel(),
         _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
     _check(st, "kvq_paged_prefill_attention")
+
+
+def _rows(t, name, rows, heads, d):
+    """(pointer, row stride) of fp16 rows [rows][heads][d] whose rows may lie
+    further apart than a row is long (a slice of a projection's output)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if tuple(t.shape) != (rows, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), heads * d if rows <= 1 else t.stride(0)
+
+
+def prompt_workspace_bytes(cfg: Config, num_seqs: int, total_tokens: int, max_seq_tokens: int,
+                           mass_window: int = 0) -> int:
+    out = _sz(0)
+    _check(load_library().kvq_prompt_workspace_bytes(ctypes.byref(cfg.c()), num_seqs, total_tokens, max_seq_tokens,
+                                                     mass_window, ctypes.byref(out)), "kvq_prompt_workspace_bytes")
+    return out.value
+
+
+def prompt_attention(cfg: Config, q, k, v, out, cu_seqlens, max_seq_tokens: int, lse=None, mass=None,
+                     mass_window: int = 0, workspace=None, softmax_scale: float | None = None, dev_status=None,
+                     stream=None) -> None:
+    """Read path, whole prompts: causal attention over packed raw rows (q
+    fp16 [N][H_q][d]; k, v fp16 [N][H_kv][d]; rows may be strided; sequences
+    by the prefix sums ``cu_seqlens``) into ``out`` fp16 [N][H_q][d] and
+    ``lse`` fp32 [N][H_q].  With ``mass`` (fp32 [B][max_tiles]) the tiles'
+    attention weight from the last ``mass_window`` tokens of each sequence (0:
+    all) is added to it; ``workspace`` is then a uint8 CUDA tensor of at least
+    ``prompt_workspace_bytes`` bytes."""
+    if softmax_scale is None:
+        softmax_scale = cfg.head_dim ** -0.5
+    n, b = q.shape[0], cu_seqlens.shape[0] - 1
+    qp, qs = _rows(q, "q", n, cfg.num_q_heads, cfg.head_dim)
+    kp, ks = _rows(k, "k", n, cfg.num_kv_heads, cfg.head_dim)
+    vp, vs = _rows(v, "v", n, cfg.num_kv_heads, cfg.head_dim)
+    if mass is not None and (mass.dim() != 2 or mass.shape[0] != b):
+        raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    st = load_library().kvq_prompt_attention(
+        ctypes.byref(cfg.c()), qp, qs, kp, ks, vp, vs,
+        _ptr(out, "out", torch.float16, (n, cfg.num_q_heads, cfg.head_dim)),
+        _ptr(lse, "lse", torch.float32, (n, cfg.num_q_heads)), _ptr(cu_seqlens, "cu_seqlens", torch.int32), b, n,
+        int(max_seq_tokens), float(softmax_scale), _ptr(mass, "mass", torch.float32),
+        0 if mass is None else mass.shape[1], int(mass_window), _ptr(workspace, "workspace", torch.uint8),
+        0 if workspace is None else workspace.numel(), _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+    _check(st, "kvq_prompt_attention")
 
 
 # bytes of the library's static decode scratch (one per device)
