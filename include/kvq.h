@@ -229,6 +229,64 @@ KVQ_API kvq_status kvq_paged_decode_attention(const kvq_config* cfg, const void*
                                       size_t workspace_bytes, int num_splits,
                                       int32_t* dev_status, void* stream);
 
+/* Bytes of device workspace kvq_paged_decode_attention_mass needs on the
+ * current device: the decode's, and 8 bytes per (sequence, tile of the block
+ * table, query head).  cfg, bytes: host pointers. */
+KVQ_API kvq_status kvq_decode_mass_workspace_bytes(const kvq_config* cfg, int num_seqs, int max_blocks_per_seq,
+                                                   int num_splits, size_t* bytes);
+
+/* kvq_paged_decode_attention that also adds the step's attention weight to
+ * the tiles' masses.
+ *   mass         : device fp32 [num_seqs][max_tiles]: entry (s, t) grows by the
+ *                  weight that the tokens of tile t of sequence s receive,
+ *                  summed over the query heads; the raw tail counts as the
+ *                  tile that it will become.  max_tiles holds the block
+ *                  table's tiles at least (a length past max_tiles tiles is
+ *                  reported through dev_status, KVQ_ERR_DEVICE_BOUNDS).
+ *   workspace    : device, >= kvq_decode_mass_workspace_bytes(cfg, num_seqs,
+ *                  max_blocks_per_seq, num_splits) bytes; contents on entry are
+ *                  ignored.
+ * The rest as kvq_paged_decode_attention; out has the same bits for the same
+ * num_splits. */
+KVQ_API kvq_status kvq_paged_decode_attention_mass(const kvq_config* cfg, const void* q, void* out, float* mass,
+                                           int max_tiles, const int32_t* seq_lens, int num_seqs,
+                                           const int32_t* block_tables, int max_blocks_per_seq, int num_blocks,
+                                           const void* k_pool, const void* v_pool, const void* k_tail,
+                                           const void* v_tail, float softmax_scale, void* workspace,
+                                           size_t workspace_bytes, int num_splits, int32_t* dev_status,
+                                           void* stream);
+
+/* Bytes of device workspace kvq_evict_tiles needs.  cfg, bytes: host pointers. */
+KVQ_API kvq_status kvq_evict_workspace_bytes(const kvq_config* cfg, int num_seqs, int max_blocks_per_seq,
+                                             size_t* bytes);
+
+/* Eviction by accumulated attention weight: every sequence with more than
+ * keep_tiles full tiles loses the excess, the tiles with the least mass first
+ * (equal masses: the lower index; NaN counts as the largest), except the
+ * first sink_tiles and the last recent_tiles of its full tiles.  The raw tail
+ * stays.  In place, for a sequence of n full tiles of which e leave:
+ *   block_tables : device int32 [num_seqs][max_blocks_per_seq].  The blocks of
+ *                  the kept tiles move up in order, those of the evicted tiles
+ *                  follow in order, blocks past the n tiles stay: the row
+ *                  keeps its blocks, and the next tiles that the sequence
+ *                  fills take the evicted ones.
+ *   seq_lens     : device int32 [num_seqs], less e * tile_tokens.
+ *   mass         : device fp32 [num_seqs][max_tiles]: the kept tiles' entries,
+ *                  then the tail's (entry n before), then zeros.
+ *   kept         : device int32 [num_seqs][max_tiles] or NULL: the old index of
+ *                  every kept tile, then -1 (also for sequences that lose none).
+ *   keep_tiles   : >= sink_tiles + recent_tiles, all >= 0.
+ *   workspace    : device, >= kvq_evict_workspace_bytes(...) bytes; contents on
+ *                  entry are ignored.  Calls that overlap in time need one each.
+ * Tokens keep the positions their rows were rotated with; a caller that
+ * derives positions from lengths counts evicted tokens itself.  A sequence
+ * with more full tiles than its block-table row or mass row holds is left as
+ * it was and reported through dev_status (KVQ_ERR_DEVICE_BOUNDS). */
+KVQ_API kvq_status kvq_evict_tiles(const kvq_config* cfg, float* mass, int max_tiles, int keep_tiles,
+                                   int sink_tiles, int recent_tiles, int32_t* seq_lens, int num_seqs,
+                                   int32_t* block_tables, int max_blocks_per_seq, int32_t* kept, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_status, void* stream);
+
 /* One serving step in one launch (d = 128; three at d = 64 / 256): append one
  * token per sequence and decode.
  * The pages say the per-step read path decides the serving gain (aitrends.kr

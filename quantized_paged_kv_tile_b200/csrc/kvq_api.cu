@@ -81,6 +81,53 @@ kvq_status check_tables(const int32_t* block_tables, int max_blocks_per_seq, int
   return KVQ_OK;
 }
 
+// The checks of the decode calls in the order they report; fills *a.
+kvq_status check_decode(const kvq_config* cfg, const void* q, void* out, const int32_t* seq_lens, int num_seqs,
+                        const int32_t* block_tables, int max_blocks_per_seq, int num_blocks, const void* k_pool,
+                        const void* v_pool, const void* k_tail, const void* v_tail, float softmax_scale,
+                        void* workspace, int num_splits, int32_t* dev_status, kvq::DecodeArgs* a) {
+  KVQ_TRY(check_config(cfg));
+  if (num_seqs < 0 || num_splits < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs or num_splits");
+  if (num_seqs == 0) return KVQ_OK;
+  if (num_seqs > 65535) return fail(KVQ_ERR_INVALID_ARG, "num_seqs > 65535");
+  if (!(softmax_scale > 0.f) || !(softmax_scale < 1e30f))
+    return fail(KVQ_ERR_INVALID_ARG, "softmax_scale must be a positive finite float");
+  KVQ_TRY(check_ptr(q, "q"));
+  KVQ_TRY(check_ptr(out, "out"));
+  KVQ_TRY(check_ptr(seq_lens, "seq_lens"));
+  KVQ_TRY(check_tables(block_tables, max_blocks_per_seq, num_blocks));
+  KVQ_TRY(check_ptr(k_pool, "k_pool"));
+  KVQ_TRY(check_ptr(v_pool, "v_pool"));
+  KVQ_TRY(check_ptr(k_tail, "k_tail"));
+  KVQ_TRY(check_ptr(v_tail, "v_tail"));
+  KVQ_TRY(check_ptr(workspace, "workspace"));
+  KVQ_TRY(check_ptr(dev_status, "dev_status", true));
+  if (num_splits > 65535) return fail(KVQ_ERR_INVALID_ARG, "num_splits > 65535");
+  // the device counts work units in 32-bit ints: (num_seqs x num_kv_heads) x (splits + 2) stays below 2^30
+  if (static_cast<long long>(num_seqs) * cfg->num_kv_heads * (num_splits + 2) >= (1LL << 30))
+    return fail(KVQ_ERR_INVALID_ARG, "num_seqs x num_kv_heads x num_splits too large (%d x %d x %d)", num_seqs,
+                cfg->num_kv_heads, num_splits);
+  a->cfg = *cfg;
+  a->gk = kvq::pool_geom(*cfg, false);
+  a->gv = kvq::pool_geom(*cfg, true);
+  a->q = q;
+  a->out = out;
+  a->seq_lens = seq_lens;
+  a->num_seqs = num_seqs;
+  a->block_tables = block_tables;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->num_blocks = num_blocks;
+  a->k_pool = k_pool;
+  a->v_pool = v_pool;
+  a->k_tail = k_tail;
+  a->v_tail = v_tail;
+  a->softmax_scale = softmax_scale;
+  a->workspace = workspace;
+  a->num_splits_fixed = num_splits;
+  a->dev_status = dev_status;
+  return KVQ_OK;
+}
+
 kvq_status check_prompt_sizes(const kvq_config* cfg, int num_seqs, int total_tokens, int max_seq_tokens,
                               int mass_window) {
   if (num_seqs < 0 || total_tokens < 0 || max_seq_tokens < 0 || mass_window < 0)
@@ -237,53 +284,105 @@ kvq_status kvq_paged_decode_attention(const kvq_config* cfg, const void* q, void
                                       int num_blocks, const void* k_pool, const void* v_pool, const void* k_tail,
                                       const void* v_tail, float softmax_scale, void* workspace,
                                       size_t workspace_bytes, int num_splits, int32_t* dev_status, void* stream) {
-  KVQ_TRY(check_config(cfg));
-  if (num_seqs < 0 || num_splits < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs or num_splits");
+  kvq::DecodeArgs a{};
+  KVQ_TRY(check_decode(cfg, q, out, seq_lens, num_seqs, block_tables, max_blocks_per_seq, num_blocks, k_pool, v_pool,
+                       k_tail, v_tail, softmax_scale, workspace, num_splits, dev_status, &a));
   if (num_seqs == 0) return ok();
-  if (num_seqs > 65535) return fail(KVQ_ERR_INVALID_ARG, "num_seqs > 65535");
-  if (!(softmax_scale > 0.f) || !(softmax_scale < 1e30f))
-    return fail(KVQ_ERR_INVALID_ARG, "softmax_scale must be a positive finite float");
-  KVQ_TRY(check_ptr(q, "q"));
-  KVQ_TRY(check_ptr(out, "out"));
-  KVQ_TRY(check_ptr(seq_lens, "seq_lens"));
-  KVQ_TRY(check_tables(block_tables, max_blocks_per_seq, num_blocks));
-  KVQ_TRY(check_ptr(k_pool, "k_pool"));
-  KVQ_TRY(check_ptr(v_pool, "v_pool"));
-  KVQ_TRY(check_ptr(k_tail, "k_tail"));
-  KVQ_TRY(check_ptr(v_tail, "v_tail"));
-  KVQ_TRY(check_ptr(workspace, "workspace"));
-  KVQ_TRY(check_ptr(dev_status, "dev_status", true));
-  if (num_splits > 65535) return fail(KVQ_ERR_INVALID_ARG, "num_splits > 65535");
-  // the device counts work units in 32-bit ints: (num_seqs x num_kv_heads) x (splits + 2) stays below 2^30
-  if (static_cast<long long>(num_seqs) * cfg->num_kv_heads * (num_splits + 2) >= (1LL << 30))
-    return fail(KVQ_ERR_INVALID_ARG, "num_seqs x num_kv_heads x num_splits too large (%d x %d x %d)", num_seqs,
-                cfg->num_kv_heads, num_splits);
   int sms = 0;
   if (num_splits == 0) KVQ_TRY(device_sm_count(&sms));
   const size_t need = kvq::decode_workspace_bytes(*cfg, num_seqs, num_splits, sms);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  return cuda_status(kvq::launch_paged_decode(a, static_cast<cudaStream_t>(stream)),
+                     "kvq_paged_decode_attention launch");
+}
+
+kvq_status kvq_decode_mass_workspace_bytes(const kvq_config* cfg, int num_seqs, int max_blocks_per_seq,
+                                           int num_splits, size_t* bytes) {
+  KVQ_TRY(check_config(cfg));
+  if (bytes == nullptr) return fail(KVQ_ERR_INVALID_ARG, "bytes output is NULL");
+  if (num_seqs < 0 || num_splits < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs or num_splits");
+  if (max_blocks_per_seq < 1) return fail(KVQ_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
+  int sms = 0;
+  KVQ_TRY(device_sm_count(&sms));
+  *bytes = kvq::decode_mass_workspace_bytes(*cfg, num_seqs, max_blocks_per_seq, num_splits, sms);
+  return ok();
+}
+
+kvq_status kvq_paged_decode_attention_mass(const kvq_config* cfg, const void* q, void* out, float* mass,
+                                           int max_tiles, const int32_t* seq_lens, int num_seqs,
+                                           const int32_t* block_tables, int max_blocks_per_seq, int num_blocks,
+                                           const void* k_pool, const void* v_pool, const void* k_tail,
+                                           const void* v_tail, float softmax_scale, void* workspace,
+                                           size_t workspace_bytes, int num_splits, int32_t* dev_status,
+                                           void* stream) {
   kvq::DecodeArgs a{};
+  KVQ_TRY(check_decode(cfg, q, out, seq_lens, num_seqs, block_tables, max_blocks_per_seq, num_blocks, k_pool, v_pool,
+                       k_tail, v_tail, softmax_scale, workspace, num_splits, dev_status, &a));
+  if (num_seqs == 0) return ok();
+  KVQ_TRY(check_ptr(mass, "mass"));
+  const int pages = cfg->tile_tokens / cfg->page_tokens;
+  if (max_tiles < (max_blocks_per_seq + pages - 1) / pages)
+    return fail(KVQ_ERR_INVALID_ARG, "max_tiles %d is less than the block table's %d", max_tiles,
+                (max_blocks_per_seq + pages - 1) / pages);
+  int sms = 0;
+  KVQ_TRY(device_sm_count(&sms));
+  const size_t need = kvq::decode_mass_workspace_bytes(*cfg, num_seqs, max_blocks_per_seq, num_splits, sms);
+  if (workspace_bytes < need)
+    return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  a.mass = mass;
+  a.mass_tiles = max_tiles;
+  return cuda_status(kvq::launch_paged_decode_mass(a, static_cast<cudaStream_t>(stream)),
+                     "kvq_paged_decode_attention_mass launch");
+}
+
+kvq_status kvq_evict_workspace_bytes(const kvq_config* cfg, int num_seqs, int max_blocks_per_seq, size_t* bytes) {
+  KVQ_TRY(check_config(cfg));
+  if (bytes == nullptr) return fail(KVQ_ERR_INVALID_ARG, "bytes output is NULL");
+  if (num_seqs < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs");
+  if (max_blocks_per_seq < 1) return fail(KVQ_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
+  *bytes = kvq::evict_workspace_bytes(*cfg, num_seqs, max_blocks_per_seq);
+  return ok();
+}
+
+kvq_status kvq_evict_tiles(const kvq_config* cfg, float* mass, int max_tiles, int keep_tiles, int sink_tiles,
+                           int recent_tiles, int32_t* seq_lens, int num_seqs, int32_t* block_tables,
+                           int max_blocks_per_seq, int32_t* kept, void* workspace, size_t workspace_bytes,
+                           int32_t* dev_status, void* stream) {
+  KVQ_TRY(check_config(cfg));
+  if (num_seqs < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs");
+  if (max_tiles < 1) return fail(KVQ_ERR_INVALID_ARG, "max_tiles must be >= 1 (got %d)", max_tiles);
+  if (sink_tiles < 0 || recent_tiles < 0 || keep_tiles < 0)
+    return fail(KVQ_ERR_INVALID_ARG, "negative keep_tiles, sink_tiles or recent_tiles");
+  if (sink_tiles > keep_tiles || recent_tiles > keep_tiles - sink_tiles)
+    return fail(KVQ_ERR_INVALID_ARG, "keep_tiles %d is less than sink_tiles %d + recent_tiles %d", keep_tiles,
+                sink_tiles, recent_tiles);
+  if (num_seqs == 0) return ok();
+  if (num_seqs > 65535) return fail(KVQ_ERR_INVALID_ARG, "num_seqs > 65535");
+  KVQ_TRY(check_ptr(mass, "mass"));
+  KVQ_TRY(check_ptr(seq_lens, "seq_lens"));
+  KVQ_TRY(check_tables(block_tables, max_blocks_per_seq, 1));
+  KVQ_TRY(check_ptr(kept, "kept", true));
+  KVQ_TRY(check_ptr(workspace, "workspace"));
+  KVQ_TRY(check_ptr(dev_status, "dev_status", true));
+  const size_t need = kvq::evict_workspace_bytes(*cfg, num_seqs, max_blocks_per_seq);
+  if (workspace_bytes < need)
+    return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  kvq::EvictArgs a{};
   a.cfg = *cfg;
-  a.gk = kvq::pool_geom(*cfg, false);
-  a.gv = kvq::pool_geom(*cfg, true);
-  a.q = q;
-  a.out = out;
+  a.mass = mass;
+  a.max_tiles = max_tiles;
+  a.keep_tiles = keep_tiles;
+  a.sink_tiles = sink_tiles;
+  a.recent_tiles = recent_tiles;
   a.seq_lens = seq_lens;
   a.num_seqs = num_seqs;
   a.block_tables = block_tables;
   a.max_blocks_per_seq = max_blocks_per_seq;
-  a.num_blocks = num_blocks;
-  a.k_pool = k_pool;
-  a.v_pool = v_pool;
-  a.k_tail = k_tail;
-  a.v_tail = v_tail;
-  a.softmax_scale = softmax_scale;
+  a.kept = kept;
   a.workspace = workspace;
-  a.num_splits_fixed = num_splits;
   a.dev_status = dev_status;
-  return cuda_status(kvq::launch_paged_decode(a, static_cast<cudaStream_t>(stream)),
-                     "kvq_paged_decode_attention launch");
+  return cuda_status(kvq::launch_evict_tiles(a, static_cast<cudaStream_t>(stream)), "kvq_evict_tiles launch");
 }
 
 kvq_status kvq_append_decode_step(const kvq_config* cfg, const void* new_k, const void* new_v, const void* q,

@@ -355,6 +355,15 @@ __host__ __device__ inline GenDecSmem gen_dec_smem(int D, int T) {
   return m;
 }
 
+// a tile's share of the softmax of head hh of pair (b, h): its sum of weights
+// and the maximum they are relative to (calls with masses only)
+__device__ __forceinline__ void store_tile_stats(const DecodeArgs& a, int pair, int tile, int hh, float l, float m) {
+  if (tile >= a.mass_stat_tiles) return;
+  const int nh = a.cfg.num_kv_heads, G = a.cfg.group_size;
+  const size_t row = static_cast<size_t>(pair / nh) * a.mass_stat_tiles + tile;
+  a.mass_stats[(row * nh + pair % nh) * G + hh] = make_float2(l, m);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kGThreads) gen_decode_split_kernel(DecodeArgs a, int S) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -417,7 +426,10 @@ __global__ void __launch_bounds__(kGThreads) gen_decode_split_kernel(DecodeArgs 
     __syncthreads();
     const bool tile_ok = ok;
     __syncthreads();  // every thread has read ok before thread 0 writes the next tile's
-    if (!tile_ok) continue;  // tile skipped (reported)
+    if (!tile_ok) {  // tile skipped (reported)
+      if (a.mass_stats != nullptr && tid < G) store_tile_stats(a, pair, tile, tid, 0.f, 0.f);
+      continue;
+    }
     // codes, metadata and C~ of the tile
     for (int idx = tid; idx < T * D; idx += kGThreads) {
       const int i = idx / D, j = idx % D, k = i / kPageTokens, p = i % kPageTokens;
@@ -478,6 +490,7 @@ __global__ void __launch_bounds__(kGThreads) gen_decode_split_kernel(DecodeArgs 
         hs[8 * hh + 1] = hs[8 * hh + 1] * alpha + ls;
         hs[8 * hh + 2] = alpha;
         hs[8 * hh + 4] = wz;
+        if (a.mass_stats != nullptr) store_tile_stats(a, pair, tile, hh, ls, m_new);
       }
     }
     __syncthreads();
@@ -575,6 +588,11 @@ __global__ void __launch_bounds__(kGThreads) gen_decode_merge_kernel(DecodeArgs 
       hs[8 * hh + 2] = mm;
       hs[8 * hh + 3] = ls + et * hs[8 * hh + 1];
       hs[8 * hh + 4] = et;
+      if (a.mass_stats != nullptr) {  // the head's final statistics, and the tail's share as its tile to be
+        const float ltot = hs[8 * hh + 3];
+        a.mass_final[static_cast<size_t>(pair) * G + hh] = make_float2(mm, ltot > 0.f ? 1.f / ltot : 0.f);
+        if (tau > 0) store_tile_stats(a, pair, L / T, hh, hs[8 * hh + 1], hs[8 * hh]);
+      }
     }
   }
   __syncthreads();

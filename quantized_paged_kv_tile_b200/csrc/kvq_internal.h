@@ -112,10 +112,39 @@ struct DecodeArgs {
   const void* new_k;       // [B][H_kv][d] fp16
   const void* new_v;
   int32_t* seq_lens_rw;    // the same array as seq_lens, written at the end of the step
+  // masses (kvq_paged_decode_attention_mass); null otherwise
+  float* mass;             // [B][mass_tiles]
+  int mass_tiles;
+  int mass_stat_tiles;     // tiles per sequence in mass_stats
+  float2* mass_stats;      // workspace [B][mass_stat_tiles][H_q]: sum and maximum of a tile's weights
+  float2* mass_final;      // workspace [B][H_q]: final maximum and 1 / sum
 };
 // Workspace bytes for a split setting on a device with num_sms SMs.
 size_t decode_workspace_bytes(const kvq_config& cfg, int num_seqs, int num_splits, int num_sms);
 cudaError_t launch_paged_decode(const DecodeArgs& a, cudaStream_t s);
+// the same decode, the tiles' attention weight added to a.mass; its workspace
+// is the decode's and the statistics behind it
+int decode_mass_stat_tiles(const kvq_config& cfg, int max_blocks_per_seq);
+size_t decode_mass_workspace_bytes(const kvq_config& cfg, int num_seqs, int max_blocks_per_seq, int num_splits,
+                                   int sms);
+cudaError_t launch_paged_decode_mass(DecodeArgs a, cudaStream_t s);
+
+// Eviction: the tiles with the least mass out of the block tables.
+struct EvictArgs {
+  kvq_config cfg;
+  float* mass;             // [B][max_tiles]
+  int max_tiles;
+  int keep_tiles, sink_tiles, recent_tiles;
+  int32_t* seq_lens;       // [B]
+  int num_seqs;
+  int32_t* block_tables;   // [B][max_blocks_per_seq]
+  int max_blocks_per_seq;
+  int32_t* kept;           // [B][max_tiles], may be null
+  void* workspace;
+  int32_t* dev_status;
+};
+size_t evict_workspace_bytes(const kvq_config& cfg, int num_seqs, int max_blocks_per_seq);
+cudaError_t launch_evict_tiles(const EvictArgs& a, cudaStream_t s);
 // the fused serving step: one launch (append one token per sequence, decode,
 // advance the lengths); the workspace counters must be zero on entry and are
 // left zero

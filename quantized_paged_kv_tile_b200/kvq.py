@@ -32,6 +32,8 @@ EXPORTED_SYMBOLS = (
     "kvq_selftest_bounded_wait", "kvq_status_string", "kvq_last_error", "kvq_version",
     "kvq_prefill_workspace_bytes", "kvq_paged_prefill_attention", "kvq_append_decode_step",
     "kvq_prompt_workspace_bytes", "kvq_prompt_attention",
+    "kvq_decode_mass_workspace_bytes", "kvq_paged_decode_attention_mass", "kvq_evict_workspace_bytes",
+    "kvq_evict_tiles",
 )
 
 
@@ -106,6 +108,11 @@ _SIGNATURES = {
     "kvq_prompt_workspace_bytes": [_cfgp, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)],
     "kvq_prompt_attention": [_cfgp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp,
                              _i32, _i32, _vp, _sz, _vp, _vp],
+    "kvq_decode_mass_workspace_bytes": [_cfgp, _i32, _i32, _i32, ctypes.POINTER(_sz)],
+    "kvq_paged_decode_attention_mass": [_cfgp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
+                                        _f32, _vp, _sz, _i32, _vp, _vp],
+    "kvq_evict_workspace_bytes": [_cfgp, _i32, _i32, ctypes.POINTER(_sz)],
+    "kvq_evict_tiles": [_cfgp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _sz, _vp, _vp],
     "kvq_unpack_tiles": [_cfgp, _vp, _i32, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
 }
 
@@ -234,6 +241,64 @@ def paged_decode_attention(cfg: Config, q, out, seq_lens, block_tables, k_pool, 
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), num_splits,
         _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
     _check(st, "kvq_paged_decode_attention")
+
+
+def decode_mass_workspace_bytes(cfg: Config, num_seqs: int, max_blocks_per_seq: int, num_splits: int = 0) -> int:
+    out = _sz(0)
+    _check(load_library().kvq_decode_mass_workspace_bytes(ctypes.byref(cfg.c()), num_seqs, max_blocks_per_seq,
+                                                          num_splits, ctypes.byref(out)),
+           "kvq_decode_mass_workspace_bytes")
+    return out.value
+
+
+def paged_decode_attention_mass(cfg: Config, q, out, mass, seq_lens, block_tables, k_pool, v_pool, k_tail, v_tail,
+                                workspace, softmax_scale: float | None = None, num_splits: int = 0,
+                                num_blocks: int | None = None, dev_status=None, stream=None) -> None:
+    """``paged_decode_attention`` that adds the step's attention weight to the
+    tiles' masses (``mass`` fp32 [B][max_tiles]); ``workspace`` is a uint8
+    CUDA tensor of at least ``decode_mass_workspace_bytes`` bytes."""
+    if softmax_scale is None:
+        softmax_scale = cfg.head_dim ** -0.5
+    nb = k_pool.shape[0] if num_blocks is None else num_blocks
+    b = seq_lens.shape[0]
+    if mass.dim() != 2 or mass.shape[0] != b:
+        raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    st = load_library().kvq_paged_decode_attention_mass(
+        ctypes.byref(cfg.c()), _ptr(q, "q", torch.float16), _ptr(out, "out", torch.float16),
+        _ptr(mass, "mass", torch.float32), mass.shape[1], _ptr(seq_lens, "seq_lens", torch.int32), b,
+        _ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1], nb,
+        _ptr(k_pool, "k_pool", torch.uint8), _ptr(v_pool, "v_pool", torch.uint8),
+        _ptr(k_tail, "k_tail", torch.float16), _ptr(v_tail, "v_tail", torch.float16), float(softmax_scale),
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), num_splits,
+        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+    _check(st, "kvq_paged_decode_attention_mass")
+
+
+def evict_workspace_bytes(cfg: Config, num_seqs: int, max_blocks_per_seq: int) -> int:
+    out = _sz(0)
+    _check(load_library().kvq_evict_workspace_bytes(ctypes.byref(cfg.c()), num_seqs, max_blocks_per_seq,
+                                                    ctypes.byref(out)), "kvq_evict_workspace_bytes")
+    return out.value
+
+
+def evict_tiles(cfg: Config, mass, seq_lens, block_tables, keep_tiles: int, sink_tiles: int = 0,
+                recent_tiles: int = 0, kept=None, workspace=None, dev_status=None, stream=None) -> None:
+    """Evict the tiles with the least mass (``mass`` fp32 [B][max_tiles]) of
+    every sequence with more than ``keep_tiles`` full tiles, except its first
+    ``sink_tiles`` and last ``recent_tiles``: ``block_tables``, ``seq_lens`` and
+    ``mass`` are compacted in place; ``kept`` (int32 [B][max_tiles], optional)
+    gets the kept tiles' old indices.  ``workspace``: uint8, at least
+    ``evict_workspace_bytes`` bytes."""
+    b = seq_lens.shape[0]
+    if mass.dim() != 2 or mass.shape[0] != b:
+        raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    st = load_library().kvq_evict_tiles(
+        ctypes.byref(cfg.c()), _ptr(mass, "mass", torch.float32), mass.shape[1], int(keep_tiles), int(sink_tiles),
+        int(recent_tiles), _ptr(seq_lens, "seq_lens", torch.int32), b,
+        _ptr(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1])), block_tables.shape[1],
+        _ptr(kept, "kept", torch.int32, tuple(mass.shape)), _ptr(workspace, "workspace", torch.uint8),
+        0 if workspace is None else workspace.numel(), _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+    _check(st, "kvq_evict_tiles")
 
 
 def append_decode_step(cfg: Config, new_k, new_v, q, out, seq_lens, block_tables, k_pool, v_pool, k_tail, v_tail,

@@ -9,6 +9,10 @@ turns user-level operations into the three library calls:
   decode(q)      -> kvq_paged_decode_attention
   prefill_chunk(q, rows) -> kvq_paged_prefill_attention over the cache and
                     the chunk, then kvq_append_tokens of the chunk
+  prompt(q, rows) -> kvq_prompt_attention over raw prompts, then prefill(rows)
+  evict(keep)    -> kvq_evict_tiles (caches that track masses)
+With ``track_mass=True`` prompt() and decode() also add the attention weight
+that every tile receives to ``mass`` (kvq_paged_decode_attention_mass).
 All arithmetic runs in the library's kernels; this module only sizes and
 indexes buffers (PyTorch provides the memory and the stream).
 """
@@ -47,7 +51,7 @@ def _in_use(buf):
 
 class PagedKVCache:
     def __init__(self, cfg: kvq.Config, num_seqs: int, max_tokens_per_seq: int, device="cuda",
-                 block_table: np.ndarray | None = None, num_splits: int = 0):
+                 block_table: np.ndarray | None = None, num_splits: int = 0, track_mass: bool = False):
         self.cfg = cfg
         self.num_seqs = num_seqs
         self.device = torch.device(device)
@@ -70,10 +74,29 @@ class PagedKVCache:
         self.seq_lens = torch.zeros(num_seqs, dtype=torch.int32, device=self.device)
         self.host_lens = np.zeros(num_seqs, dtype=np.int64)
         self.num_splits = num_splits
-        self.workspace = torch.empty(kvq.decode_workspace_bytes(cfg, num_seqs, num_splits), dtype=torch.uint8,
-                                     device=self.device)
+        # accumulated attention weight per tile, fp32 [B][max_tiles] (None: not tracked)
+        self.max_tiles = -(-self.blocks_per_seq * cfg.page_tokens // cfg.tile_tokens)
+        self.mass = torch.zeros((num_seqs, self.max_tiles), dtype=torch.float32,
+                                device=self.device) if track_mass else None
+        self.workspace = torch.empty(self._decode_bytes(num_splits), dtype=torch.uint8, device=self.device)
+        self.prompt_workspace = None  # grown on demand by prompt when it tracks masses
+        self.evict_workspace = None
         self.prefill_workspace = None  # grown on demand by prefill_chunk when it splits contexts
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _decode_bytes(self, num_splits: int) -> int:
+        if self.mass is None:
+            return kvq.decode_workspace_bytes(self.cfg, self.num_seqs, num_splits)
+        return kvq.decode_mass_workspace_bytes(self.cfg, self.num_seqs, self.blocks_per_seq, num_splits)
+
+    def _run_decode(self, q, out, workspace, num_splits, mass) -> None:
+        """The decode call on the current stream, with masses into ``mass`` if given."""
+        args = (self.seq_lens, self.block_tables, self.k_pool, self.v_pool, self.k_tail, self.v_tail, workspace)
+        kw = dict(num_splits=num_splits, num_blocks=self.num_blocks, dev_status=self.dev_status)
+        if mass is None:
+            kvq.paged_decode_attention(self.cfg, q, out, *args, **kw)
+        else:
+            kvq.paged_decode_attention_mass(self.cfg, q, out, mass, *args, **kw)
 
     # ------------------------------------------------------------------ write
     def prefill_tile_desc(self, lens) -> np.ndarray:
@@ -133,15 +156,72 @@ class PagedKVCache:
             if out is None:
                 out = torch.empty_like(q)
             ws = self.workspace
-            need = kvq.decode_workspace_bytes(self.cfg, self.num_seqs, splits)
+            need = self._decode_bytes(splits)
             if ws.numel() < need:
                 ws = torch.empty(need, dtype=torch.uint8, device=self.device)  # freed after this call's work
             else:
                 _in_use(ws)
-            kvq.paged_decode_attention(self.cfg, q, out, self.seq_lens, self.block_tables, self.k_pool,
-                                       self.v_pool, self.k_tail, self.v_tail, ws, num_splits=splits,
-                                       num_blocks=self.num_blocks, dev_status=self.dev_status)
+            _in_use(self.mass)
+            self._run_decode(q, out, ws, splits, self.mass)
         return out
+
+    def prompt(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens, out: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None, mass_window: int = 0, stream=None) -> torch.Tensor:
+        """Whole prompts into an empty cache: causal attention of the packed rows
+        (``lens`` tokens per sequence; q fp16 [N][H_q][d], k / v fp16
+        [N][H_kv][d], rows may be strided) over themselves, then ``prefill`` of
+        the same rows.  With ``track_mass`` the tiles' masses grow by the weight
+        from the last ``mass_window`` tokens of each prompt (0: all).  Returns
+        out fp16 [N][H_q][d]; ``lse`` fp32 [N][H_q] is filled if given."""
+        lens = np.asarray(lens, dtype=np.int64)
+        if lens.shape != (self.num_seqs,) or np.any(lens < 0):
+            raise ValueError("lens: one non-negative prompt length per sequence")
+        if int(lens.sum()) != q.shape[0]:
+            raise ValueError(f"lens sum to {int(lens.sum())}, q has {q.shape[0]} rows")
+        if np.any(self.host_lens):
+            raise RuntimeError("prompt expects an empty cache")
+        if np.any(lens > self.blocks_per_seq * self.cfg.page_tokens):
+            raise ValueError("prompt past the allocated pages")
+        if mass_window and self.mass is None:
+            raise ValueError("mass_window needs a cache with track_mass")
+        longest = int(lens.max()) if lens.size else 0
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            cu = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(self.device)
+            ws = None
+            if self.mass is not None:
+                need = kvq.prompt_workspace_bytes(self.cfg, self.num_seqs, q.shape[0], longest, mass_window)
+                if self.prompt_workspace is None or self.prompt_workspace.numel() < need:
+                    self.prompt_workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+                ws = self.prompt_workspace
+                _in_use(ws)
+                _in_use(self.mass)
+            kvq.prompt_attention(self.cfg, q, k, v, out, cu, longest, lse=lse, mass=self.mass,
+                                 mass_window=mass_window, workspace=ws, dev_status=self.dev_status)
+            self.prefill(k.contiguous(), v.contiguous(), lens)
+        return out
+
+    # --------------------------------------------------------------- eviction
+    def evict(self, keep_tiles: int, sink_tiles: int = 1, recent_tiles: int = 1, kept: torch.Tensor | None = None,
+              stream=None) -> None:
+        """Bring every sequence down to ``keep_tiles`` full tiles: those with the
+        least mass leave, never the first ``sink_tiles`` or the last
+        ``recent_tiles``.  Lengths shrink; rows keep the positions they were
+        rotated with.  ``kept`` (int32 [B][max_tiles]) gets the old indices of
+        the kept tiles."""
+        if self.mass is None:
+            raise ValueError("evict needs a cache with track_mass")
+        t = self.cfg.tile_tokens
+        with _on_stream(stream):
+            if self.evict_workspace is None:
+                need = kvq.evict_workspace_bytes(self.cfg, self.num_seqs, self.blocks_per_seq)
+                self.evict_workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=self.device)
+            _in_use(self.evict_workspace)
+            _in_use(self.mass)
+            kvq.evict_tiles(self.cfg, self.mass, self.seq_lens, self.block_tables, keep_tiles, sink_tiles,
+                            recent_tiles, kept=kept, workspace=self.evict_workspace, dev_status=self.dev_status)
+        self.host_lens = self.host_lens - np.maximum(0, self.host_lens // t - keep_tiles) * t
 
     def prefill_chunk(self, q: torch.Tensor, new_k: torch.Tensor, new_v: torch.Tensor, counts,
                       out: torch.Tensor | None = None, append: bool = True, num_splits: int | None = None,
@@ -151,7 +231,8 @@ class PagedKVCache:
         cached context and causally to their own chunk; then (``append``) the
         chunk joins the cache.  ``num_splits`` (default: chosen from the
         context lengths and the SM count) splits long contexts over more
-        CTAs.  Returns out fp16 [N][H_q][d]."""
+        CTAs.  Returns out fp16 [N][H_q][d].  The chunk's queries do not add to
+        the masses of a cache that tracks them."""
         counts = np.asarray(counts, dtype=np.int64)
         if counts.shape != (self.num_seqs,) or np.any(counts < 0):
             raise ValueError("counts: one non-negative chunk length per sequence")
@@ -212,12 +293,15 @@ class DecodeStepGraph:
     decode, the lengths advanced); steps that complete a tile replay the
     append + decode graph (the completed tile has to be quantized first).
     Both use the same split count, so the outputs are those of the unfused
-    step bit for bit.
+    step bit for bit.  A cache that tracks masses takes the unfused step, whose
+    decode adds to them; ``evict`` between replays needs no new capture.
     """
 
     def __init__(self, cache: PagedKVCache, num_splits: int | None = None, fused: bool = False):
         self.cache = cache
         cfg, b, dev = cache.cfg, cache.num_seqs, cache.device
+        if fused and cache.mass is not None:
+            raise ValueError("the one-launch step does not track masses: use fused=False")
         self.fused = fused
         if fused and num_splits is None:
             num_splits = kvq.step_splits(cfg, b, torch.cuda.get_device_properties(dev).multi_processor_count)
@@ -227,7 +311,7 @@ class DecodeStepGraph:
         self.q = torch.zeros((b, cfg.num_q_heads, cfg.head_dim), dtype=torch.float16, device=dev)
         self.out = torch.empty_like(self.q)
         self._cu = torch.arange(b + 1, dtype=torch.int32, device=dev)
-        need = kvq.decode_workspace_bytes(cfg, b, self.num_splits)
+        need = cache._decode_bytes(self.num_splits)
         if cache.workspace.numel() < need:
             cache.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         # the fused step's own workspace: zero-filled once, left zero by every step
@@ -236,8 +320,9 @@ class DecodeStepGraph:
         side = torch.cuda.Stream(device=dev)
         side.wait_stream(torch.cuda.current_stream(dev))
         with torch.cuda.stream(side):
-            # the decode once eagerly on the current contents (no state change)
-            self._decode()
+            # the decode once eagerly on the current contents (no state change:
+            # masses, if tracked, go to a copy)
+            self._decode(None if cache.mass is None else cache.mass.clone())
         torch.cuda.current_stream(dev).wait_stream(side)
         torch.cuda.synchronize(dev)
         with torch.cuda.graph(self.graph):
@@ -248,18 +333,15 @@ class DecodeStepGraph:
             with torch.cuda.graph(self.graph_fused):
                 self._fused_step()
 
-    def _decode(self) -> None:
-        c = self.cache
-        kvq.paged_decode_attention(c.cfg, self.q, self.out, c.seq_lens, c.block_tables, c.k_pool, c.v_pool,
-                                   c.k_tail, c.v_tail, c.workspace, num_splits=self.num_splits,
-                                   num_blocks=c.num_blocks, dev_status=c.dev_status)
+    def _decode(self, mass) -> None:
+        self.cache._run_decode(self.q, self.out, self.cache.workspace, self.num_splits, mass)
 
     def _step(self) -> None:
         c = self.cache
         kvq.append_tokens(c.cfg, self.new_k, self.new_v, self._cu, c.seq_lens, 1, c.block_tables, c.k_pool,
                           c.v_pool, c.k_tail, c.v_tail, num_blocks=c.num_blocks, dev_status=c.dev_status)
         c.seq_lens.add_(1)
-        self._decode()
+        self._decode(c.mass)
 
     def _fused_step(self) -> None:
         c = self.cache
