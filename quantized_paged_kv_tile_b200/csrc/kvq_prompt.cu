@@ -42,21 +42,24 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kRows = 128;    // query rows per unit (TMEM lanes)
-constexpr int kKeys = 128;    // keys per tile
-constexpr int kThreads = 128;
+constexpr int kRows = 128;    // query rows per query tile (TMEM lanes)
+// The running maximum a row's weights are relative to follows the true one
+// only once that is more than 2^kLazy larger: weights reach 2^8 then (fp16 and
+// the fp32 sums hold that as exactly as 1), and O is rescaled rarely.
+constexpr float kLazy = 8.f;
 // up to this many sequences the units are taken longest first
 constexpr int kSortedSeqs = 1024;
 
 struct PromptDev {
   PromptArgs a;
-  int unit_tokens;     // query tokens per unit
+  int tile_tokens;     // query tokens per query tile
+  int unit_tokens;     // query tokens per unit (one or two query tiles)
   int units;           // host bound on the number of units
   int max_tiles_k;     // key tiles of the longest sequence
-  int window_units;    // units per (sequence, head) that can hold counted queries; 0: all
+  int window_runs;     // query tiles per (sequence, head) that can hold counted queries; 0: all
   float qscale;        // softmax_scale * log2 e
-  float* scratch;      // per CTA [max_tiles_k][kKeys / T + 1][kRows]
-  float* part;         // per unit [max_tiles_k * kKeys / T]
+  float* scratch;      // per CTA and query tile [max_tiles_k][entries per key tile + 1][kRows]
+  float* part;         // per query tile of the call [max_tiles_k * entries per key tile]
 };
 
 // Length and first row of sequence s; 0 tokens if the prefix sums are bad.
@@ -132,322 +135,609 @@ __device__ Unit locate_unit(const PromptDev& pd, int u, int lane) {
   return r;
 }
 
-// slot of a unit in the partial masses; -1: none of its queries counts
-__device__ __forceinline__ long long mass_slot(const PromptDev& pd, const Unit& u) {
+// slot of query tile `run` of u's sequence and head in the partial masses; -1:
+// none of its queries counts
+__device__ __forceinline__ long long mass_slot(const PromptDev& pd, const Unit& u, int run) {
   const PromptArgs& a = pd.a;
-  const int W = pd.unit_tokens;
-  if (a.mass_window == 0)
-    return (static_cast<long long>(u.first / W + u.seq + u.run)) * a.cfg.num_kv_heads + u.head;
-  const int r0 = max(0, u.n - a.mass_window) / W;
-  if (u.run < r0) return -1;
-  return (static_cast<long long>(u.seq) * pd.window_units + (u.run - r0)) * a.cfg.num_kv_heads + u.head;
+  const int W1 = pd.tile_tokens;
+  if (a.mass_window == 0) return (static_cast<long long>(u.first / W1 + u.seq + run)) * a.cfg.num_kv_heads + u.head;
+  const int r0 = max(0, u.n - a.mass_window) / W1;
+  if (run < r0) return -1;
+  return (static_cast<long long>(u.seq) * pd.window_runs + (run - r0)) * a.cfg.num_kv_heads + u.head;
 }
 
+__device__ __forceinline__ float max3f(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
+
+// Shapes per head size.  kQT query tiles of 128 rows share the key tiles that
+// the CTA loads, one softmax warpgroup each; TMEM holds two score tiles and
+// kQT output tiles.
 template <int D>
 struct Geom {
-  static constexpr int kQ = 0;                          // Q: 128 rows x D, 64-channel blocks of 16 KB
-  static constexpr int kK = kQ + kRows * D * 2;         // K tile: 128 keys x D
-  static constexpr int kV = kK + kKeys * D * 2;         // V tile: 128 keys x D
-  static constexpr int kStat = kV + kKeys * D * 2;      // float m[128], w[128]
-  static constexpr int kBar = kStat + 2 * kRows * 4;    // mbarriers: q, kv, mma
-  static constexpr int kMisc = kBar + 32;               // TMEM slot, stop flag, non-finite V flag, unit
-  static constexpr int kSmem = kMisc + 64 + 1024;       // + alignment slack
+  static constexpr int kQT = D == 256 ? 1 : 2;
+  static constexpr int kKeys = D == 256 ? 64 : 128;      // keys per tile
+  static constexpr int kSlot = kKeys * D * 2;            // one K or V tile
+  static constexpr int kSlots = D == 64 ? 8 : (D == 128 ? 4 : 5);
+  static constexpr int kSoftmax = kQT * 128;             // softmax threads
+  static constexpr int kThreads = kSoftmax + 128;        // + MMA, load, V guard and unit warps
+  static constexpr int kQTile = kRows * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kKV = kQ + kQT * kQTile;
+  static constexpr int kStat = kKV + kSlots * kSlot;     // float m[128], w[128] per query tile (masses)
+  static constexpr int kBar = kStat + kQT * 2 * kRows * 4;
+  static constexpr int kMisc = kBar + 256;
+  static constexpr int kSmem = kMisc + 128 + 1024;       // + alignment slack
+  static_assert(kSmem <= 232448, "shared memory per block");
+  // TMEM columns
+  static constexpr int kS = 0, kO = 2 * kKeys;
+  static_assert(kO + kQT * D <= 512, "TMEM columns");
 };
 
+// mbarriers, 8 bytes each, from Geom::kBar on
+enum : int {
+  kBarQFull = 0,   // the unit's Q tiles have landed
+  kBarQEmpty,      // its last score MMA has read them
+  kBarS,           // [2] a score tile is in TMEM
+  kBarP = kBarS + 2,    // [2] its P is in TMEM (one arrival per softmax warp)
+  kBarO = kBarP + 2,    // [2] the PV MMA of a query tile is done
+  kBarG = kBarO + 2,    // V of an edge tile has landed: the guard may look at it
+  kBarV,                // the guard is done with it
+  kBarUFull,            // [2] a unit is published
+  kBarUEmpty = kBarUFull + 2,  // [2] every warp is done with it
+  kBarDrain = kBarUEmpty + 2,
+  kBarKVFull,           // [kSlots]
+  kBarCount = kBarKVFull + 8 + 8
+};
+static_assert(kBarCount * 8 <= 256, "barriers fit");
+
+struct Shared {  // at Geom::kMisc
+  uint32_t tmem;
+  int stop;
+  int odd_v[2];   // per unit slot: V values of an edge tile were left out
+  Unit unit[2];
+};
+
+// mbar_wait by a whole warp, with one answer for its lanes
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(kFull, mbar_wait(bar, parity, stop));
+}
+
+// A running position in a ring of barriers
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// The key tiles of a unit's query tile q: tokens [i0 + q W1, ...) of n
+__device__ __forceinline__ int key_tiles(int i0, int q, int W1, int n, int keys) {
+  const int first = i0 + q * W1;
+  return first < n ? (min(n, first + W1) + keys - 1) / keys : 0;
+}
+
 template <int D, bool MASS>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(const __grid_constant__ CUtensorMap mq,
-                                                          const __grid_constant__ CUtensorMap mk,
-                                                          const __grid_constant__ CUtensorMap mv, PromptDev pd) {
+__global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap mq,
+                                                                      const __grid_constant__ CUtensorMap mk,
+                                                                      const __grid_constant__ CUtensorMap mv,
+                                                                      const __grid_constant__ PromptDev pd) {
   using Geo = Geom<D>;
+  constexpr int QT = Geo::kQT, KT = Geo::kKeys, NS = Geo::kSlots;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const PromptArgs& a = pd.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = a.cfg.group_size, nh = a.cfg.num_kv_heads, T = a.cfg.tile_tokens;
-  const int W = pd.unit_tokens, row = tid;
-  const uint32_t s0 = smem_u32(smem), bar_q = s0 + Geo::kBar, bar_kv = bar_q + 8, bar_mma = bar_q + 16;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + Geo::kMisc);
-  volatile int* stop = reinterpret_cast<volatile int*>(smem + Geo::kMisc + 4);
-  int* odd_v = reinterpret_cast<int*>(smem + Geo::kMisc + 8);
-  Unit* s_unit = reinterpret_cast<Unit*>(smem + Geo::kMisc + 16);
-  float* s_m = reinterpret_cast<float*>(smem + Geo::kStat);
-  float* s_w = s_m + kRows;
+  const int G = a.cfg.group_size, nh = a.cfg.num_kv_heads;
+  const int W1 = pd.tile_tokens;  // query tokens per query tile
+  const uint32_t s0 = smem_u32(smem), bars = s0 + Geo::kBar;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  Shared* sh = reinterpret_cast<Shared*>(smem + Geo::kMisc);
+  volatile int* stop = &sh->stop;
 
-  // rows of the Q tile that no box fills (g not a divisor of 128) stay zero
-  for (int i = tid; i < kRows * D * 2 / 16; i += kThreads)
+  // rows of the Q tiles that no box fills (g not a divisor of 128) stay zero
+  for (int i = tid; i < QT * Geo::kQTile / 16; i += Geo::kThreads)
     reinterpret_cast<uint4*>(smem + Geo::kQ)[i] = make_uint4(0, 0, 0, 0);
   fence_async_smem();
   if (tid == 0) {
-    mbar_init(bar_q, 1);
-    mbar_init(bar_kv, 1);
-    mbar_init(bar_mma, 1);
+    mbar_init(bar(kBarQFull), 1);
+    mbar_init(bar(kBarQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarS + i), 1);
+      mbar_init(bar(kBarP + i), 4);
+      mbar_init(bar(kBarO + i), 1);
+      mbar_init(bar(kBarUFull + i), 1);
+      mbar_init(bar(kBarUEmpty + i), 4 * QT + 3);
+    }
+    mbar_init(bar(kBarG), 1);
+    mbar_init(bar(kBarV), 1);
+    mbar_init(bar(kBarDrain), 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(kBarKVFull + i), 1);
+      mbar_init(bar(kBarKVFull + NS + i), 1);
+    }
     mbar_init_fence();
-    *stop = 0;
-    *odd_v = 0;
+    sh->stop = 0;
   }
-  if (warp == 0) tmem_alloc512(smem_u32(tslot));
+  if (warp == 0) tmem_alloc512(smem_u32(&sh->tmem));
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tm = *tslot, tS = tm, tO = tm + kKeys;  // S (and P over it): 128 columns; O: D columns
-  const uint32_t tlane = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t tm = sh->tmem;
 
-  if (blockIdx.x == 0) {
-    for (int s = tid; s < a.num_seqs; s += kThreads) {
-      const int f = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-      if (f < 0 || e < f || e > a.total_tokens || e - f > a.max_seq_tokens)
-        report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
-    }
-  }
-
-  uint32_t ph_q = 0, ph_kv = 0, ph_mma = 0;
-  bool failed = false;
-  const int sub_n = kKeys / T;
-  for (int round = 0; !failed; ++round) {
-    const long long ul = static_cast<long long>(round) * gridDim.x +
-                         ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (ul >= pd.units) break;
-    if (warp == 0) {
-      const Unit u = locate_unit(pd, static_cast<int>(ul), lane);
-      if (lane == 0) *s_unit = u;
-    }
-    __syncthreads();
-    const Unit u = *s_unit;
-    __syncthreads();
-    if (u.n == 0) {
-      if (a.num_seqs <= kSortedSeqs) break;
-      continue;
-    }
-    const int i0 = u.run * W, i1 = min(u.n, i0 + W);  // query tokens [i0, i1)
-    const int nk = (i1 + kKeys - 1) / kKeys;          // key tiles
-    const int edge = i0 / kKeys;                      // tiles from here on hold keys that some row does not see
-    const int ti = i0 + row / G;                      // this row's token
-    const bool live = row < W * G && ti < u.n;
-    const int vis = live ? ti : i1 - 1;               // last key this row sees
-    const long long slot = MASS ? mass_slot(pd, u) : -1;
-    float* scr = pd.scratch + static_cast<size_t>(blockIdx.x) * pd.max_tiles_k * (sub_n + 1) * kRows;
-    float m = -INFINITY, l = 0.f;
-    if (tid == 0) {
-      mbar_expect_tx(bar_q, W * G * D * 2);
-      for (int c = 0; c < D / 64; ++c)
-        tma_load(s0 + Geo::kQ + c * kRows * 128, &mq, 64 * c, u.head * G, u.first + i0, bar_q);
-    }
-    for (int j = 0; j < nk; ++j) {
-      if (tid == 0) {
-        mbar_expect_tx(bar_kv, 2 * kKeys * D * 2);
-        for (int c = 0; c < D / 64; ++c) {
-          tma_load(s0 + Geo::kK + c * kKeys * 128, &mk, 64 * c, u.head, u.first + j * kKeys, bar_kv);
-          tma_load(s0 + Geo::kV + c * kKeys * 128, &mv, 64 * c, u.head, u.first + j * kKeys, bar_kv);
+  if (warp >= 4 * QT) {
+    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    const int role = warp - 4 * QT;
+    if (role == 3) {
+      // ------------------------------------------------------------ units
+      if (blockIdx.x == 0) {
+        for (int s = lane; s < a.num_seqs; s += 32) {
+          const int f = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
+          if (f < 0 || e < f || e > a.total_tokens || e - f > a.max_seq_tokens)
+            report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
         }
       }
-      bool ok = j > 0 || mbar_wait(bar_q, ph_q, stop);
-      ok = ok && mbar_wait(bar_kv, ph_kv, stop);
-      if (__syncthreads_or(!ok)) {
-        failed = true;
-        break;
+      Ring r;
+      for (int round = 0;; ++round) {
+        const long long ul = static_cast<long long>(round) * gridDim.x +
+                             ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        Unit u{0, 0, 0, -1, 0};  // n = -1: no more
+        if (ul < pd.units) {
+          u = locate_unit(pd, static_cast<int>(ul), lane);
+          if (u.n == 0) {
+            if (a.num_seqs > kSortedSeqs) continue;
+            u.n = -1;
+          }
+        }
+        if (!warp_wait(bar(kBarUEmpty + r.slot), r.phase ^ 1u, stop)) break;
+        if (lane == 0) {
+          sh->unit[r.slot] = u;
+          sh->odd_v[r.slot] = 0;
+          mbar_arrive(bar(kBarUFull + r.slot));
+        }
+        r.next(2);
+        if (u.n < 0) break;
       }
-      ph_kv ^= 1;
-      if (tid == 0) {
-        fence_after();
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tS, sw128_desc(s0 + Geo::kQ + (k >> 2) * kRows * 128 + (k & 3) * 32, 0),
-                 sw128_desc(s0 + Geo::kK + (k >> 2) * kKeys * 128 + (k & 3) * 32, 0), idesc_m128(kKeys, false), k != 0);
-        mma_commit(bar_mma);
-      }
-      if (j >= edge) {
-        // V of a tile with masked keys: rows past the sequence and values that
-        // are not finite become zero (the latter are added at the end)
-        for (int i = tid; i < kKeys * D / 8; i += kThreads) {
-          const int key = (i >> 3) % kKeys;
-          uint4* p = reinterpret_cast<uint4*>(smem + Geo::kV) + i;
-          uint4 x = *p;
-          if (j * kKeys + key >= u.n) {
-            *p = make_uint4(0, 0, 0, 0);
-          } else {
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            bool odd = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((w[e] & 0x7C00u) == 0x7C00u) { w[e] &= 0xFFFF0000u; odd = true; }
-              if ((w[e] & 0x7C000000u) == 0x7C000000u) { w[e] &= 0x0000FFFFu; odd = true; }
+    } else if (role == 1) {
+      // ------------------------------------------------------------ loads
+      if (lane == 0) {
+        Ring ru, kv;
+        uint32_t ph_q = 0;
+        bool ok = true;
+        int issued = 0;
+        while (ok) {
+          if (!mbar_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
+          const Unit u = sh->unit[ru.slot];
+          mbar_arrive(bar(kBarUEmpty + ru.slot));
+          ru.next(2);
+          if (u.n < 0) break;
+          const int i0 = u.run * W1 * QT;
+          int nk = 0;
+          for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles(i0, q, W1, u.n, KT));
+          if (!(ok = mbar_wait(bar(kBarQEmpty), ph_q ^ 1u, stop))) break;
+          ph_q ^= 1u;
+          mbar_expect_tx(bar(kBarQFull), QT * W1 * G * D * 2);
+          for (int q = 0; q < QT; ++q)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load(s0 + Geo::kQ + q * Geo::kQTile + c * kRows * 128, &mq, 64 * c, u.head * G,
+                       u.first + i0 + q * W1, bar(kBarQFull));
+          for (int t = 0; t < 2 * nk && ok; ++t) {
+            if (!(ok = mbar_wait(bar(kBarKVFull + NS + kv.slot), kv.phase ^ 1u, stop))) break;
+            mbar_expect_tx(bar(kBarKVFull + kv.slot), Geo::kSlot);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load(s0 + Geo::kKV + kv.slot * Geo::kSlot + c * KT * 128, (t & 1) ? &mv : &mk, 64 * c, u.head,
+                       u.first + (t >> 1) * KT, bar(kBarKVFull + kv.slot));
+            kv.next(NS);
+            issued = min(issued + 1, NS);
+          }
+        }
+        if (*stop) {  // copies in flight land before the shared memory is given back
+          const long long t0 = global_ns();
+          for (int i = 0; i < issued; ++i) {
+            kv.slot = kv.slot == 0 ? NS - 1 : kv.slot - 1;
+            if (kv.slot == NS - 1) kv.phase ^= 1u;
+            while (!mbar_try(bar(kBarKVFull + kv.slot), kv.phase) && global_ns() - t0 < kWaitLimitNs) {
             }
-            if (odd) {
-              *p = x;
-              *odd_v = 1;
+          }
+          while (issued > 0 && !mbar_try(bar(kBarQFull), ph_q ^ 1u) && global_ns() - t0 < kWaitLimitNs) {
+          }
+        }
+      }
+    } else if (role == 0) {
+      // ------------------------------------------------------------ matrix instructions
+      if (lane == 0) {
+        Ring ru, kv;
+        uint32_t ph_q = 0, ph_p[2] = {0u, 0u}, ph_v = 0;
+        bool ok = true;
+        // S[buf] = Q_q K^T with K in slot `slot`
+        auto score = [&](int q, int buf, int slot) {
+          const uint32_t qa = s0 + Geo::kQ + q * Geo::kQTile, ka = s0 + Geo::kKV + slot * Geo::kSlot;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tm + Geo::kS + buf * KT, sw128_desc(qa + (k >> 2) * kRows * 128 + (k & 3) * 32, 0),
+                   sw128_desc(ka + (k >> 2) * KT * 128 + (k & 3) * 32, 0), idesc_m128(KT, false), k != 0);
+          mma_commit(bar(kBarS + buf));
+        };
+        // O_q (+)= P[buf] V with V in slot `slot`
+        auto value = [&](int q, int buf, int slot, bool acc) {
+          const uint32_t va = s0 + Geo::kKV + slot * Geo::kSlot;
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            mma_ts(tm + Geo::kO + q * D, tm + Geo::kS + buf * KT + 8 * k, sw128_desc(va + k * 2048, KT * 128),
+                   idesc_m128(D, true), acc || k > 0);
+          mma_commit(bar(kBarO + q));
+        };
+        auto wait_kv = [&] {
+          const bool r = mbar_wait(bar(kBarKVFull + kv.slot), kv.phase, stop);
+          fence_after();
+          return r;
+        };
+        auto wait_p = [&](int buf) {
+          const bool r = mbar_wait(bar(kBarP + buf), ph_p[buf], stop);
+          ph_p[buf] ^= 1u;
+          fence_after();
+          return r;
+        };
+        while (ok) {
+          if (!mbar_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
+          const Unit u = sh->unit[ru.slot];
+          mbar_arrive(bar(kBarUEmpty + ru.slot));
+          ru.next(2);
+          if (u.n < 0) break;
+          const int i0 = u.run * W1 * QT, edge = i0 / KT;
+          int nkq[2] = {key_tiles(i0, 0, W1, u.n, KT), QT == 2 ? key_tiles(i0, 1, W1, u.n, KT) : 0};
+          const int nk = max(nkq[0], nkq[1]);
+          if (!(ok = mbar_wait(bar(kBarQFull), ph_q, stop))) break;
+          ph_q ^= 1u;
+          if (!(ok = wait_kv())) break;  // K of tile 0
+          score(0, 0, kv.slot);
+          if (QT == 2 && nkq[1] > 0) score(1, 1, kv.slot);
+          mma_commit(bar(kBarKVFull + NS + kv.slot));
+          if (nk == 1) mma_commit(bar(kBarQEmpty));
+          kv.next(NS);
+          for (int j = 0; j < nk && ok; ++j) {
+            const Ring v = kv;
+            Ring k2 = kv;  // K of tile j + 1
+            k2.next(NS);
+            if (!(ok = wait_kv())) break;
+            bool guarded = j >= edge;  // the guard looks at V while the softmax of the tile runs
+            if (guarded) mbar_arrive(bar(kBarG));
+            auto wait_guard = [&] {
+              if (!guarded) return true;
+              guarded = false;
+              const bool r = mbar_wait(bar(kBarV), ph_v, stop);
+              ph_v ^= 1u;
+              fence_after();
+              return r;
+            };
+            kv.next(NS);
+            if constexpr (QT == 2) {
+              bool have_k = false;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                if (j >= nkq[q]) continue;
+                if (!(ok = wait_p(q) && wait_guard())) break;
+                value(q, q, v.slot, j > 0);
+                if (j + 1 < nkq[q]) {
+                  if (!have_k && !(ok = wait_kv())) break;
+                  have_k = true;
+                  score(q, q, k2.slot);
+                }
+              }
+            } else {
+              if (j + 1 < nk) {
+                if (!(ok = wait_kv())) break;
+                score(0, (j + 1) & 1, k2.slot);
+              }
+              if (!(ok = wait_p(j & 1) && wait_guard())) break;
+              value(0, j & 1, v.slot, j > 0);
+            }
+            if (!ok) break;
+            mma_commit(bar(kBarKVFull + NS + v.slot));
+            if (j + 1 < nk) {
+              mma_commit(bar(kBarKVFull + NS + k2.slot));
+              if (j + 2 == nk) mma_commit(bar(kBarQEmpty));
+              kv.next(NS);
             }
           }
         }
-        fence_async_smem();
-      }
-      ok = mbar_wait(bar_mma, ph_mma, stop);
-      if (__syncthreads_or(!ok)) {
-        failed = true;
-        break;
-      }
-      ph_mma ^= 1;
-      fence_after();
-
-      float s[kKeys];
-      tmem_ld32<0>(tS + tlane, s);
-      tmem_ld32<32>(tS + tlane + 32, s);
-      tmem_ld32<64>(tS + tlane + 64, s);
-      tmem_ld32<96>(tS + tlane + 96, s);
-      tmem_wait32<0>(s);
-      tmem_wait32<32>(s);
-      tmem_wait32<64>(s);
-      tmem_wait32<96>(s);
-      if (j >= edge) {
-        const int lim = vis - j * kKeys;
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
-      }
-      float mx = s[0];
-#pragma unroll
-      for (int c = 1; c < kKeys; ++c) mx = fmaxf(mx, s[c]);
-      const float m_old = m;
-      m = fmaxf(m, mx * pd.qscale);
-      const float mu = m == -INFINITY ? 0.f : m;  // a row with no finite score so far
-      const float alpha = ex2(m_old - mu);
-      l *= alpha;
-      uint32_t p[kKeys / 2];
-      float part[4] = {0.f, 0.f, 0.f, 0.f};  // sums of 32 keys
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 2) {
-        const float p0 = ex2(fmaf(s[c], pd.qscale, -mu)), p1 = ex2(fmaf(s[c + 1], pd.qscale, -mu));
-        part[c / 32] += p0 + p1;
-        p[c / 2] = h2_as_u32(__floats2half2_rn(p0, p1));
-      }
-      l += (part[0] + part[1]) + (part[2] + part[3]);
-      if (MASS && slot >= 0) {
-        float* q = scr + static_cast<size_t>(j) * (sub_n + 1) * kRows + row;
-        if (T == 32) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) q[k * kRows] = part[k];
-        } else if (T == 64) {
-          q[0] = part[0] + part[1];
-          q[kRows] = part[2] + part[3];
-        } else {
-          q[0] = (part[0] + part[1]) + (part[2] + part[3]);
+        if (*stop) {  // matrix instructions in flight end before TMEM is freed
+          mma_commit(bar(kBarDrain));
+          const long long t0 = global_ns();
+          while (!mbar_try(bar(kBarDrain), 0) && global_ns() - t0 < kWaitLimitNs) {
+          }
         }
-        q[sub_n * kRows] = mu;
       }
-      tmem_st32<0>(tS + tlane, p);
-      tmem_st32<32>(tS + tlane + 32, p);
-      if (j > 0 && __any_sync(kFull, alpha != 1.f)) {
+    } else {
+      // ------------------------------------------------------------ V guard
+      // V of the tiles that hold keys some row does not see: rows past the
+      // sequence and values that are not finite become zero
+      Ring ru, kv;
+      uint32_t ph_g = 0;
+      while (warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) {
+        const Unit u = sh->unit[ru.slot];
+        const int uslot = ru.slot;
+        ru.next(2);
+        if (u.n < 0) break;
+        const int i0 = u.run * W1 * QT, edge = i0 / KT;
+        int nk = 0;
+        for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles(i0, q, W1, u.n, KT));
+        bool ok = true;
+        for (int j = 0; j < nk; ++j) {
+          kv.next(NS);  // K
+          if (j >= edge) {
+            if (!(ok = warp_wait(bar(kBarG), ph_g, stop))) break;
+            ph_g ^= 1u;
+            uint4* p = reinterpret_cast<uint4*>(smem + Geo::kKV + kv.slot * Geo::kSlot);
+            bool odd = false;
+#pragma unroll 4
+            for (int i = lane; i < Geo::kSlot / 16; i += 32) {
+              const int key = j * KT + ((i >> 3) % KT);
+              uint4 x = p[i];
+              if (key >= u.n) {
+                p[i] = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+              bool bad = false;
 #pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((w[e] & 0x7C00u) == 0x7C00u) { w[e] &= 0xFFFF0000u; bad = true; }
+                if ((w[e] & 0x7C000000u) == 0x7C000000u) { w[e] &= 0x0000FFFFu; bad = true; }
+              }
+              if (bad) {
+                p[i] = x;
+                odd = true;
+              }
+            }
+            if (odd) sh->odd_v[uslot] = 1;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarV));
+          }
+          kv.next(NS);  // V
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int q = warp >> 2, row = tid & 127;
+    const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tO = tm + Geo::kO + q * D + tlane;
+    const int T = a.cfg.tile_tokens, wid = min(T, KT), ent = KT / wid;  // keys per mass entry, entries per tile
+    float* s_m = reinterpret_cast<float*>(smem + Geo::kStat) + q * 2 * kRows;
+    float* s_w = s_m + kRows;
+    Ring ru;
+    uint32_t ph_s[2] = {0u, 0u}, ph_o = 0;
+    while (true) {
+      if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
+      const Unit u = sh->unit[ru.slot];
+      const int uslot = ru.slot;
+      ru.next(2);
+      if (u.n < 0) break;
+      const int first = u.run * W1 * QT + q * W1;        // the tile's first token
+      const int nk = key_tiles(first, 0, W1, u.n, KT);
+      const int ti = first + row / G;                    // this row's token
+      const bool live = row < W1 * G && ti < u.n;
+      const int vis = live ? ti : u.n - 1;               // last key this row sees
+      const int masked = first / KT;                     // tiles from here on need the mask
+      const long long slot = MASS && nk > 0 ? mass_slot(pd, u, u.run * QT + q) : -1;
+      float* scr = pd.scratch + (static_cast<size_t>(blockIdx.x) * QT + q) * pd.max_tiles_k * (ent + 1) * kRows + row;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nk; ++j) {
+        const int buf = QT == 2 ? q : j & 1;
+        const uint32_t tS = tm + Geo::kS + buf * KT + tlane;
+        if (!(ok = warp_wait(bar(kBarS + buf), ph_s[buf], stop))) break;
+        ph_s[buf] ^= 1u;
+        fence_after();
+        float s[KT];
+        tmem_ld32<0>(tS, s);
+        tmem_ld32<32>(tS + 32, s);
+        if constexpr (KT == 128) {
+          tmem_ld32<KT - 64>(tS + 64, s);
+          tmem_ld32<KT - 32>(tS + 96, s);
+        }
+        tmem_wait32<0>(s);
+        tmem_wait32<32>(s);
+        if constexpr (KT == 128) {
+          tmem_wait32<KT - 64>(s);
+          tmem_wait32<KT - 32>(s);
+        }
+        if (j >= masked) {
+          const int lim = vis - j * KT;
+#pragma unroll
+          for (int c = 0; c < KT; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < KT; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = c + 4 + e < KT ? max3f(mx[e], s[c + e], s[c + 4 + e]) : fmaxf(mx[e], s[c + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * pd.qscale;
+        const bool grow = top > m + kLazy;  // (m = -inf before the first finite score)
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2(m - top);
+          m = top;
+          l *= alpha;
+        }
+        if (j > 0 && __any_sync(kFull, grow)) {
+          if constexpr (QT == 1) {  // (with two query tiles this score tile's MMA came after that PV)
+            if (!(ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop))) break;
+            fence_after();
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32<0>(tO + c, o);
+            tmem_wait32<0>(o);
+            uint32_t x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * alpha);
+            tmem_st32<0>(tO + c, x);
+          }
+        }
+        const float mu = m == -INFINITY ? 0.f : m;  // a row with no finite score so far
+        const float2 sc2 = make_float2(pd.qscale, pd.qscale), mu2 = make_float2(-mu, -mu);
+        float2 part[KT / 32];  // sums of 32 keys
+#pragma unroll
+        for (int h = 0; h < KT / 64; ++h) {
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float2 x = __ffma2_rn(make_float2(s[64 * h + c], s[64 * h + c + 1]), sc2, mu2);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            float2& sum = part[2 * h + c / 32];
+            sum = c % 32 == 0 ? e : __fadd2_rn(sum, e);
+            p[c / 2] = h2_as_u32(__float22half2_rn(e));
+          }
+          tmem_st32<0>(tS + 32 * h, p);
+        }
+        tmem_wait_st();
+        fence_before();
+        if constexpr (QT == 1) {  // one PV outstanding at most, so that a phase of kBarO is never passed over
+          if (j > 0 && !(ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop))) break;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + buf));
+        ph_o ^= 1u;
+        float ps[KT / 32];
+        float all = 0.f;
+#pragma unroll
+        for (int k = 0; k < KT / 32; ++k) all += ps[k] = part[k].x + part[k].y;
+        l += all;
+        if (MASS && slot >= 0) {
+          float* d = scr + static_cast<size_t>(j) * (ent + 1) * kRows;
+          if (wid == 32) {
+#pragma unroll
+            for (int k = 0; k < KT / 32; ++k) d[k * kRows] = ps[k];
+          } else if (wid == 64) {
+#pragma unroll
+            for (int k = 0; k < KT / 64; ++k) d[k * kRows] = ps[2 * k] + ps[2 * k + 1];
+          } else {
+            d[0] = all;
+          }
+          d[ent * kRows] = mu;
+        }
+      }
+      if (!ok) break;
+      if (nk > 0) {
+        // ---- the tile's rows
+        if (!warp_wait(bar(kBarO + q), ph_o ^ 1u, stop)) break;
+        fence_after();
+        const bool odd = *static_cast<volatile int*>(&sh->odd_v[uslot]) != 0;
+        const float inv = 1.f / l;
+        const size_t orow = static_cast<size_t>(u.first + (live ? ti : 0)) * nh * G + u.head * G + row % G;
+        __half* out = static_cast<__half*>(a.out) + orow * D;
+#pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          tmem_ld32<0>(tO + tlane + c, o);
+          tmem_ld32<0>(tO + c, o);
           tmem_wait32<0>(o);
-          uint32_t x[32];
+          if (!live) continue;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * alpha);
-          tmem_st32<0>(tO + tlane + c, x);
-        }
-      }
-      tmem_wait_st();
-      fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        fence_after();
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tO, tS + 8 * k, sw128_desc(s0 + Geo::kV + k * 2048, kKeys * 128), idesc_m128(D, true), j > 0 || k > 0);
-        mma_commit(bar_mma);
-      }
-      ok = mbar_wait(bar_mma, ph_mma, stop);
-      if (__syncthreads_or(!ok)) {
-        failed = true;
-        break;
-      }
-      ph_mma ^= 1;
-      fence_after();
-    }
-    if (failed) break;
-    ph_q ^= 1;
-
-    // ---- the unit's rows
-    const bool odd = *odd_v != 0;
-    const float inv = 1.f / l;
-    const size_t orow = (static_cast<size_t>(u.first + (live ? ti : 0)) * nh * G + u.head * G + row % G);
-    __half* out = static_cast<__half*>(a.out) + orow * D;
-#pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      float o[32];
-      tmem_ld32<0>(tO + tlane + c, o);
-      tmem_wait32<0>(o);
-      if (!live) continue;
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (odd) {  // the values the V guard left out, to the rows that see them
+            for (int key = u.run * W1 * QT / KT * KT; key <= vis; ++key) {
+              const __half* vr = static_cast<const __half*>(a.v) + static_cast<size_t>(u.first + key) * a.v_stride +
+                                 u.head * D + c;
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] *= inv;
-      if (odd) {  // the values left out above, to the rows that see them
-        for (int key = edge * kKeys; key <= vis; ++key) {
-          const __half* vr = static_cast<const __half*>(a.v) + static_cast<size_t>(u.first + key) * a.v_stride +
-                             u.head * D + c;
+              for (int e = 0; e < 32; ++e) {
+                const float x = __half2float(vr[e]);
+                if (!(fabsf(x) <= 65504.f)) o[e] += x;
+              }
+            }
+          }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = __half2float(vr[e]);
-            if (!(fabsf(x) <= 65504.f)) o[e] += x;
+          for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = h2_as_u32(__floats2half2_rn(o[e], o[e + 1]));
+            w.y = h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3]));
+            w.z = h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5]));
+            w.w = h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7]));
+            *reinterpret_cast<uint4*>(out + c + e) = w;
           }
         }
+        if (live && a.lse != nullptr) a.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+        if (MASS && slot >= 0) {
+          const bool counts = live && (a.mass_window == 0 || ti >= u.n - a.mass_window);
+          s_m[row] = m == -INFINITY ? 0.f : m;
+          s_w[row] = counts ? inv : 0.f;
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+          float* dst = pd.part + static_cast<size_t>(slot) * pd.max_tiles_k * ent;
+          const float* base = scr - row;
+          for (int i = row; i < nk * ent; i += kRows) {
+            const float* psum = base + (static_cast<size_t>(i / ent) * (ent + 1) + i % ent) * kRows;
+            const float* pm = base + (static_cast<size_t>(i / ent) * (ent + 1) + ent) * kRows;
+            float sum = 0.f;
+#pragma unroll 4
+            for (int r = 0; r < kRows; r += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(psum + r), y = *reinterpret_cast<const float4*>(pm + r);
+              const float4 f = *reinterpret_cast<const float4*>(s_m + r), w = *reinterpret_cast<const float4*>(s_w + r);
+              if (w.x != 0.f) sum += x.x * ex2(y.x - f.x) * w.x;
+              if (w.y != 0.f) sum += x.y * ex2(y.y - f.y) * w.y;
+              if (w.z != 0.f) sum += x.z * ex2(y.z - f.z) * w.z;
+              if (w.w != 0.f) sum += x.w * ex2(y.w - f.w) * w.w;
+            }
+            dst[i] = sum;
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
+        }
+        fence_before();
       }
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint4 w;
-        w.x = h2_as_u32(__floats2half2_rn(o[e], o[e + 1]));
-        w.y = h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3]));
-        w.z = h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5]));
-        w.w = h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7]));
-        *reinterpret_cast<uint4*>(out + c + e) = w;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
     }
-    if (live && a.lse != nullptr) a.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
-    if (MASS && slot >= 0) {
-      const bool counts = live && (a.mass_window == 0 || ti >= u.n - a.mass_window);
-      s_m[row] = m == -INFINITY ? 0.f : m;
-      s_w[row] = counts ? inv : 0.f;
-      __syncthreads();
-      float* dst = pd.part + static_cast<size_t>(slot) * pd.max_tiles_k * sub_n;
-      for (int i = tid; i < nk * sub_n; i += kThreads) {
-        const float* ps = scr + (static_cast<size_t>(i / sub_n) * (sub_n + 1) + i % sub_n) * kRows;
-        const float* pm = scr + (static_cast<size_t>(i / sub_n) * (sub_n + 1) + sub_n) * kRows;
-        float sum = 0.f;
-        for (int r = 0; r < kRows; ++r)
-          if (s_w[r] != 0.f) sum += ps[r] * ex2(pm[r] - s_m[r]) * s_w[r];
-        dst[i] = sum;
-      }
-    }
-    fence_before();
-    __syncthreads();
-    fence_after();
-    if (tid == 0) *odd_v = 0;
-  }
-  if (failed) {
-    // copies in flight land before the shared memory is given back
-    if (tid == 0) report_error(a.dev_status, KVQ_ERR_DEVICE_TIMEOUT);
-    const long long t0 = global_ns();
-    while (global_ns() - t0 < kWaitLimitNs && !mbar_try(bar_kv, ph_kv)) {
-    }
+    if (*stop && tid == 0) report_error(a.dev_status, KVQ_ERR_DEVICE_TIMEOUT);
   }
   fence_before();
   __syncthreads();
+  fence_after();
   if (warp == 0) tmem_free512(tm);
 }
 
-// mass[s][t] += the partial masses of the units of sequence s that reach tile
-// t, over heads and runs in order.  A thread per tile.
-__global__ void __launch_bounds__(128) prompt_mass_kernel(PromptDev pd) {
+// mass[s][t] += the partial masses of the query tiles of sequence s that reach
+// tile t.  A CTA per 32 tiles: lanes over the tiles, warps over the (run,
+// head) rows with a fixed stride, then the warps in order.
+constexpr int kMassWarps = 32;
+__global__ void __launch_bounds__(kMassWarps * 32) prompt_mass_kernel(PromptDev pd, int keys) {
+  __shared__ float s_sum[kMassWarps][33];
   const PromptArgs& a = pd.a;
-  const int s = blockIdx.y, t = blockIdx.x * blockDim.x + threadIdx.x;
-  const int T = a.cfg.tile_tokens, W = pd.unit_tokens, nh = a.cfg.num_kv_heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s = blockIdx.y, t = blockIdx.x * 32 + lane;
+  const int T = a.cfg.tile_tokens, W1 = pd.tile_tokens, nh = a.cfg.num_kv_heads;
+  const int wid = min(T, keys), per = T / wid;  // partial sums per tile of T
   Unit u{s, 0, 0, 0, 0};
   u.n = seq_len(a, s, u.first);
-  if (t >= (u.n + T - 1) / T || t >= a.max_tiles) return;
-  const int w0 = a.mass_window == 0 ? 0 : max(0, u.n - a.mass_window) / W;
-  const int r0 = max(w0, t * T / W), r1 = (u.n + W - 1) / W;
-  const size_t stride = static_cast<size_t>(pd.max_tiles_k) * (kKeys / T);
+  const int tiles = min((u.n + T - 1) / T, a.max_tiles);
+  if (blockIdx.x * 32 >= tiles) return;
+  const int w0 = a.mass_window == 0 ? 0 : max(0, u.n - a.mass_window) / W1;
+  const int r0 = max(w0, blockIdx.x * 32 * T / W1), rows = (u.n + W1 - 1) / W1 * nh;
+  const size_t stride = static_cast<size_t>(pd.max_tiles_k) * (keys / wid);
   float sum = 0.f;
-  for (u.run = r0; u.run < r1; ++u.run)
-    for (u.head = 0; u.head < nh; ++u.head) sum += pd.part[static_cast<size_t>(mass_slot(pd, u)) * stride + t];
-  a.mass[static_cast<size_t>(s) * a.max_tiles + t] += sum;
+#pragma unroll 4
+  for (int x = r0 * nh + warp; x < rows; x += kMassWarps) {
+    u.head = x % nh;
+    const int run = x / nh;
+    // the key tiles this query tile went over
+    const int held = (min(u.n, (run + 1) * W1) + keys - 1) / keys * (keys / wid);
+    const float* p = pd.part + static_cast<size_t>(mass_slot(pd, u, run)) * stride;
+    for (int k = 0; k < per; ++k)
+      if (t < tiles && t * per + k < held) sum += p[t * per + k];
+  }
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && t < tiles) {
+    sum = 0.f;
+    for (int w = 0; w < kMassWarps; ++w) sum += s_sum[w][lane];
+    a.mass[static_cast<size_t>(s) * a.max_tiles + t] += sum;
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -476,30 +766,34 @@ bool make_map(CUtensorMap* m, const void* base, int d, int heads, int tokens, lo
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int unit_tokens(const kvq_config& cfg) { return kRows / cfg.group_size; }
+int tile_tokens(const kvq_config& cfg) { return kRows / cfg.group_size; }
+int query_tiles(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kQT : Geom<128>::kQT; }
+int key_tile(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kKeys : Geom<128>::kKeys; }
+static_assert(Geom<64>::kQT == Geom<128>::kQT && Geom<64>::kKeys == Geom<128>::kKeys, "shapes of d = 64");
 
 struct PromptSizes {
   long long units;
-  int max_tiles_k, window_units, grid;
+  int max_tiles_k, window_runs, grid;
   size_t scratch_floats, part_floats;
 };
 PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, int max_seq_tokens, int window,
                          int sms) {
   PromptSizes z;
-  const int W = unit_tokens(cfg), sub = kKeys / cfg.tile_tokens;
-  z.units = (static_cast<long long>(total_tokens) / W + num_seqs) * cfg.num_kv_heads;
-  z.max_tiles_k = (max_seq_tokens + kKeys - 1) / kKeys;
-  z.window_units = window == 0 ? 0 : std::min((window - 1) / W + 2, (max_seq_tokens + W - 1) / W);
+  const int W1 = tile_tokens(cfg), keys = key_tile(cfg), ent = keys / std::min(keys, cfg.tile_tokens);
+  z.units = prompt_units(cfg, num_seqs, total_tokens);
+  z.max_tiles_k = (max_seq_tokens + keys - 1) / keys;
+  z.window_runs = window == 0 ? 0 : std::min((window - 1) / W1 + 2, (max_seq_tokens + W1 - 1) / W1);
   z.grid = static_cast<int>(std::min<long long>(z.units, sms));
-  z.scratch_floats = static_cast<size_t>(z.grid) * z.max_tiles_k * (sub + 1) * kRows;
-  const size_t slots = window == 0 ? static_cast<size_t>(z.units)
-                                   : static_cast<size_t>(num_seqs) * z.window_units * cfg.num_kv_heads;
-  z.part_floats = slots * z.max_tiles_k * sub;
+  z.scratch_floats = static_cast<size_t>(z.grid) * query_tiles(cfg) * z.max_tiles_k * (ent + 1) * kRows;
+  const size_t runs = window == 0 ? static_cast<size_t>(total_tokens) / W1 + num_seqs
+                                  : static_cast<size_t>(num_seqs) * z.window_runs;
+  z.part_floats = runs * cfg.num_kv_heads * z.max_tiles_k * ent;
   return z;
 }
 
 template <int D, bool MASS>
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
+  using Geo = Geom<D>;
   int dev = 0, sms = 148;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -508,33 +802,34 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   const int G = a.cfg.group_size, nh = a.cfg.num_kv_heads;
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, a.q, D, nh * G, a.total_tokens, a.q_stride, G, kRows / G) ||
-      !make_map(&mk, a.k, D, nh, a.total_tokens, a.k_stride, 1, kKeys) ||
-      !make_map(&mv, a.v, D, nh, a.total_tokens, a.v_stride, 1, kKeys))
+      !make_map(&mk, a.k, D, nh, a.total_tokens, a.k_stride, 1, Geo::kKeys) ||
+      !make_map(&mv, a.v, D, nh, a.total_tokens, a.v_stride, 1, Geo::kKeys))
     return cudaErrorInvalidValue;
   PromptDev pd{};
   pd.a = a;
-  pd.unit_tokens = unit_tokens(a.cfg);
+  pd.tile_tokens = tile_tokens(a.cfg);
+  pd.unit_tokens = pd.tile_tokens * Geo::kQT;
   pd.units = static_cast<int>(z.units);
   pd.max_tiles_k = z.max_tiles_k;
-  pd.window_units = z.window_units;
+  pd.window_runs = z.window_runs;
   pd.qscale = a.softmax_scale * kLog2e;
   pd.scratch = static_cast<float*>(a.workspace);
   pd.part = pd.scratch + z.scratch_floats;
   auto kern = prompt_kernel<D, MASS>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::kSmem);
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<z.grid, kThreads, Geom<D>::kSmem, s>>>(mq, mk, mv, pd);
+  kern<<<z.grid, Geo::kThreads, Geo::kSmem, s>>>(mq, mk, mv, pd);
   e = cudaGetLastError();
   if (e != cudaSuccess || !MASS) return e;
   const int tiles = std::min(a.max_tiles, (a.max_seq_tokens + a.cfg.tile_tokens - 1) / a.cfg.tile_tokens);
-  prompt_mass_kernel<<<dim3((tiles + 127) / 128, a.num_seqs), 128, 0, s>>>(pd);
+  prompt_mass_kernel<<<dim3((tiles + 31) / 32, a.num_seqs), kMassWarps * 32, 0, s>>>(pd, Geo::kKeys);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 long long prompt_units(const kvq_config& cfg, int num_seqs, int total_tokens) {
-  return (static_cast<long long>(total_tokens) / unit_tokens(cfg) + num_seqs) * cfg.num_kv_heads;
+  return (static_cast<long long>(total_tokens) / (tile_tokens(cfg) * query_tiles(cfg)) + num_seqs) * cfg.num_kv_heads;
 }
 
 size_t prompt_workspace_bytes(const kvq_config& cfg, int num_seqs, int total_tokens, int max_seq_tokens, int window,
