@@ -147,6 +147,15 @@ kvq_status check_row_stride(int stride, int row, const char* name) {
 
 }  // namespace
 
+cudaError_t kvq::device_sm_count(int* sms) {
+  static PerDevice known;
+  return known.get(sms, [](int* v) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
+  });
+}
+
 extern "C" {
 
 const char* kvq_status_string(kvq_status s) {
@@ -184,20 +193,12 @@ kvq_status kvq_get_layout(const kvq_config* cfg, kvq_layout* out) {
   return ok();
 }
 
-kvq_status device_sm_count(int* sms) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_status(e, "querying the SM count");
-  return KVQ_OK;
-}
-
 kvq_status kvq_decode_workspace_bytes(const kvq_config* cfg, int num_seqs, int num_splits, size_t* bytes) {
   KVQ_TRY(check_config(cfg));
   if (bytes == nullptr) return fail(KVQ_ERR_INVALID_ARG, "bytes output is NULL");
   if (num_seqs < 0 || num_splits < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs or num_splits");
   int sms = 0;
-  if (num_splits == 0) KVQ_TRY(device_sm_count(&sms));
+  if (num_splits == 0) KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
   *bytes = kvq::decode_workspace_bytes(*cfg, num_seqs, num_splits, sms);
   return ok();
 }
@@ -289,7 +290,7 @@ kvq_status kvq_paged_decode_attention(const kvq_config* cfg, const void* q, void
                        k_tail, v_tail, softmax_scale, workspace, num_splits, dev_status, &a));
   if (num_seqs == 0) return ok();
   int sms = 0;
-  if (num_splits == 0) KVQ_TRY(device_sm_count(&sms));
+  if (num_splits == 0) KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
   const size_t need = kvq::decode_workspace_bytes(*cfg, num_seqs, num_splits, sms);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -304,7 +305,7 @@ kvq_status kvq_decode_mass_workspace_bytes(const kvq_config* cfg, int num_seqs, 
   if (num_seqs < 0 || num_splits < 0) return fail(KVQ_ERR_INVALID_ARG, "negative num_seqs or num_splits");
   if (max_blocks_per_seq < 1) return fail(KVQ_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
   int sms = 0;
-  KVQ_TRY(device_sm_count(&sms));
+  KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
   *bytes = kvq::decode_mass_workspace_bytes(*cfg, num_seqs, max_blocks_per_seq, num_splits, sms);
   return ok();
 }
@@ -326,7 +327,7 @@ kvq_status kvq_paged_decode_attention_mass(const kvq_config* cfg, const void* q,
     return fail(KVQ_ERR_INVALID_ARG, "max_tiles %d is less than the block table's %d", max_tiles,
                 (max_blocks_per_seq + pages - 1) / pages);
   int sms = 0;
-  KVQ_TRY(device_sm_count(&sms));
+  KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
   const size_t need = kvq::decode_mass_workspace_bytes(*cfg, num_seqs, max_blocks_per_seq, num_splits, sms);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -532,7 +533,7 @@ kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seqs, int t
   if (bytes == nullptr) return fail(KVQ_ERR_INVALID_ARG, "bytes output is NULL");
   KVQ_TRY(check_prompt_sizes(cfg, num_seqs, total_tokens, max_seq_tokens, mass_window));
   int sms = 0;
-  KVQ_TRY(device_sm_count(&sms));
+  KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
   *bytes = kvq::prompt_workspace_bytes(*cfg, num_seqs, total_tokens, max_seq_tokens, mass_window, sms);
   return ok();
 }
@@ -566,7 +567,7 @@ kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int q_stri
   KVQ_TRY(check_ptr(dev_status, "dev_status", true));
   if (mass != nullptr) {
     int sms = 0;
-    KVQ_TRY(device_sm_count(&sms));
+    KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
     const size_t need = kvq::prompt_workspace_bytes(*cfg, num_seqs, total_tokens, max_seq_tokens, mass_window, sms);
     if (workspace_bytes < need)
       return fail(KVQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
@@ -704,7 +705,7 @@ extern "C" kvq_status kvq_paged_decode_attention_static_scratch(
   if (num_splits < 0 || num_splits > 65535)
     return fail(KVQ_ERR_INVALID_ARG, "num_splits must be 0..65535 (got %d)", num_splits);
   int sms = 0;
-  if (num_splits == 0) KVQ_TRY(device_sm_count(&sms));
+  if (num_splits == 0) KVQ_TRY(cuda_status(kvq::device_sm_count(&sms), "querying the SM count"));
   const size_t need = kvq::decode_workspace_bytes(*cfg, num_seqs, num_splits, sms);
   if (need > KVQ_DECODE_STATIC_SCRATCH_BYTES)
     return fail(KVQ_ERR_WORKSPACE,

@@ -21,12 +21,10 @@ template <int T, int BK, int BV>
 cudaError_t launch_step_bits(const DecodeArgs& a, cudaStream_t s, int sms) {
   using Geo = DecodeGeom<T, BK, BV>;
   auto kern = decode_tiles_kernel<T, BK, BV, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
-  if (e != cudaSuccess) return e;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, Geo::kWarps * 32, Geo::kSmem);
+  cudaError_t e = decode_ctas_per_sm<T, BK, BV, false>(&per_sm);
   if (e != cudaSuccess) return e;
-  kern<<<sms * std::max(per_sm, 1), Geo::kWarps * 32, Geo::kSmem, s>>>(a);
+  kern<<<sms * per_sm, Geo::kWarps * 32, Geo::kSmem, s>>>(a);
   return cudaGetLastError();
 }
 

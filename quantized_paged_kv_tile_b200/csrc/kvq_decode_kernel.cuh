@@ -1273,21 +1273,32 @@ __global__ void __launch_bounds__(DecodeGeom<T, BK, BV>::kWarps * 32, BK == 8 ? 
 
 // ------------------------------------------------------------------ launchers
 int device_sms() {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 148;
+  (void)device_sm_count(&sms);
   return sms;
+}
+
+// CTAs of the decode kernel per SM, its shared memory opted in to
+template <int T, int BK, int BV, bool MASS>
+cudaError_t decode_ctas_per_sm(int* per_sm) {
+  using Geo = DecodeGeom<T, BK, BV>;
+  static PerDevice known;
+  return known.get(per_sm, [](int* v) {
+    auto kern = decode_tiles_kernel<T, BK, BV, MASS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, Geo::kWarps * 32, Geo::kSmem);
+    *v = std::max(*v, 1);
+    return e;
+  });
 }
 
 template <int T, int BK, int BV, bool MASS>
 cudaError_t launch_decode_bits(const DecodeArgs& a, cudaStream_t s, int sms) {
   using Geo = DecodeGeom<T, BK, BV>;
   auto kern = decode_tiles_kernel<T, BK, BV, MASS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
-  if (e != cudaSuccess) return e;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, Geo::kWarps * 32, Geo::kSmem);
+  cudaError_t e = decode_ctas_per_sm<T, BK, BV, MASS>(&per_sm);
   if (e != cudaSuccess) return e;
-  per_sm = std::max(per_sm, 1);
   // automatic split: units_per_sm(T) units per SM (the warps take units from
   // a queue, so short units even out the ragged last chunks), as the
   // workspace holds

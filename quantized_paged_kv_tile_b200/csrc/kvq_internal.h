@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kvq.h"
 
 namespace kvq {
@@ -27,6 +29,32 @@ struct PoolGeom {
 };
 
 PoolGeom pool_geom(const kvq_config& cfg, bool is_v);
+
+// A number that one device and kernel instance fix, asked for once per device
+// (ordinals past the table are asked for every time).  The set-up of a launch
+// (shared-memory opt-in, occupancy) costs the host 1 to 4 us a call otherwise.
+class PerDevice {
+ public:
+  // f(int* value) -> cudaError_t
+  template <class F>
+  cudaError_t get(int* value, F&& f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kDevices;
+    if (kept && (*value = known_[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+    e = f(value);
+    if (e == cudaSuccess && kept) known_[dev].store(*value, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> known_[kDevices] = {};  // 0: not asked yet
+};
+
+// SMs of the current device
+cudaError_t device_sm_count(int* sms);
 
 // Quantize work: one item per (tile, head, K/V).
 struct QuantizeArgs {

@@ -794,9 +794,13 @@ PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, 
 template <int D, bool MASS>
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   using Geo = Geom<D>;
-  int dev = 0, sms = 148;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static PerDevice known;  // the shared memory is opted in to once per device
+  auto kern = prompt_kernel<D, MASS>;
+  int sms = 0;
+  cudaError_t e = known.get(&sms, [&](int* v) {
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+    return r != cudaSuccess ? r : device_sm_count(v);
+  });
   if (e != cudaSuccess) return e;
   const PromptSizes z = prompt_sizes(a.cfg, a.num_seqs, a.total_tokens, a.max_seq_tokens, a.mass_window, sms);
   const int G = a.cfg.group_size, nh = a.cfg.num_kv_heads;
@@ -815,9 +819,6 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   pd.qscale = a.softmax_scale * kLog2e;
   pd.scratch = static_cast<float*>(a.workspace);
   pd.part = pd.scratch + z.scratch_floats;
-  auto kern = prompt_kernel<D, MASS>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
-  if (e != cudaSuccess) return e;
   kern<<<z.grid, Geo::kThreads, Geo::kSmem, s>>>(mq, mk, mv, pd);
   e = cudaGetLastError();
   if (e != cudaSuccess || !MASS) return e;

@@ -183,9 +183,18 @@ def _ptr(t, name, dtype=None, shape=None):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without building a Stream object (3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
+
+
+def _on_current_device(*tensors) -> None:
+    """Refuse tensors (None aside) of another device than the current one: the
+    library launches on the current device."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def quantize_tiles(cfg: Config, src_k, src_v, tile_desc, block_tables, k_pool, v_pool,
@@ -263,6 +272,7 @@ def paged_decode_attention_mass(cfg: Config, q, out, mass, seq_lens, block_table
     b = seq_lens.shape[0]
     if mass.dim() != 2 or mass.shape[0] != b:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    _on_current_device(q, out, mass, seq_lens, block_tables, k_pool, v_pool, k_tail, v_tail, workspace, dev_status)
     st = load_library().kvq_paged_decode_attention_mass(
         ctypes.byref(cfg.c()), _ptr(q, "q", torch.float16), _ptr(out, "out", torch.float16),
         _ptr(mass, "mass", torch.float32), mass.shape[1], _ptr(seq_lens, "seq_lens", torch.int32), b,
@@ -292,6 +302,7 @@ def evict_tiles(cfg: Config, mass, seq_lens, block_tables, keep_tiles: int, sink
     b = seq_lens.shape[0]
     if mass.dim() != 2 or mass.shape[0] != b:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    _on_current_device(mass, seq_lens, block_tables, kept, workspace, dev_status)
     st = load_library().kvq_evict_tiles(
         ctypes.byref(cfg.c()), _ptr(mass, "mass", torch.float32), mass.shape[1], int(keep_tiles), int(sink_tiles),
         int(recent_tiles), _ptr(seq_lens, "seq_lens", torch.int32), b,
@@ -425,6 +436,7 @@ def prompt_attention(cfg: Config, q, k, v, out, cu_seqlens, max_seq_tokens: int,
     vp, vs = _rows(v, "v", n, cfg.num_kv_heads, cfg.head_dim)
     if mass is not None and (mass.dim() != 2 or mass.shape[0] != b):
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    _on_current_device(q, k, v, out, lse, cu_seqlens, mass, workspace, dev_status)
     st = load_library().kvq_prompt_attention(
         ctypes.byref(cfg.c()), qp, qs, kp, ks, vp, vs,
         _ptr(out, "out", torch.float16, (n, cfg.num_q_heads, cfg.head_dim)),
