@@ -32,6 +32,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_sm100.cuh"
@@ -148,15 +149,30 @@ __device__ __forceinline__ long long mass_slot(const PromptDev& pd, const Unit& 
 
 __device__ __forceinline__ float max3f(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
 
+// max that keeps NaN
+__device__ __forceinline__ float max3nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+#ifndef KVQ_RD
+#define KVQ_RD 88
+#define KVQ_RI 208
+#endif
+#ifndef KVQ_KT
+#define KVQ_KT 128
+#endif
 // Shapes per head size.  kQT query tiles of 128 rows share the key tiles that
 // the CTA loads, one softmax warpgroup each; TMEM holds two score tiles and
-// kQT output tiles.
+// one output tile per query tile.
 template <int D>
 struct Geom {
   static constexpr int kQT = D == 256 ? 1 : 2;
-  static constexpr int kKeys = D == 256 ? 64 : 128;      // keys per tile
+  static constexpr int kKeys = D == 256 ? 64 : KVQ_KT;   // keys per tile
+  static constexpr int kNB = kKeys == 64 ? 2 : 1;        // score tiles per query tile in TMEM
   static constexpr int kSlot = kKeys * D * 2;            // one K or V tile
-  static constexpr int kSlots = D == 64 ? 8 : (D == 128 ? 4 : 5);
+  static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 8 * 64 / kKeys : 8);
   static constexpr int kSoftmax = kQT * 128;             // softmax threads
   static constexpr int kThreads = kSoftmax + 128;        // + MMA, load, V guard and unit warps
   static constexpr int kQTile = kRows * D * 2;
@@ -164,30 +180,31 @@ struct Geom {
   static constexpr int kKV = kQ + kQT * kQTile;
   static constexpr int kStat = kKV + kSlots * kSlot;     // float m[128], w[128] per query tile (masses)
   static constexpr int kBar = kStat + kQT * 2 * kRows * 4;
-  static constexpr int kMisc = kBar + 256;
+  static constexpr int kMisc = kBar + 400;
   static constexpr int kSmem = kMisc + 128 + 1024;       // + alignment slack
   static_assert(kSmem <= 232448, "shared memory per block");
   // TMEM columns
-  static constexpr int kS = 0, kO = 2 * kKeys;
+  static constexpr int kS = 0, kO = kNB * kQT * kKeys;
   static_assert(kO + kQT * D <= 512, "TMEM columns");
 };
 
 // mbarriers, 8 bytes each, from Geom::kBar on
 enum : int {
-  kBarQFull = 0,   // the unit's Q tiles have landed
-  kBarQEmpty,      // its last score MMA has read them
-  kBarS,           // [2] a score tile is in TMEM
-  kBarP = kBarS + 2,    // [2] its P is in TMEM (one arrival per softmax warp)
-  kBarO = kBarP + 2,    // [2] the PV MMA of a query tile is done
-  kBarG = kBarO + 2,    // V of an edge tile has landed: the guard may look at it
-  kBarV,                // the guard is done with it
-  kBarUFull,            // [2] a unit is published
+  kBarQFull = 0,         // the unit's Q tiles have landed
+  kBarQEmpty,            // its last score MMA has read them
+  kBarS,                 // [2 x query tile + buffer] a score tile is in TMEM
+  kBarP = kBarS + 4,     // [same] its P is in TMEM (one arrival per softmax warp)
+  kBarH = kBarP + 4,     // [same] the first half of its P is
+  kBarO = kBarH + 4,     // [query tile + buffer] a PV MMA is done
+  kBarG = kBarO + 2,     // V of an edge tile has landed: the guard may look at it
+  kBarV,                 // the guard is done with it
+  kBarUFull,             // [2] a unit is published
   kBarUEmpty = kBarUFull + 2,  // [2] every warp is done with it
   kBarDrain = kBarUEmpty + 2,
-  kBarKVFull,           // [kSlots]
-  kBarCount = kBarKVFull + 8 + 8
+  kBarKVFull,            // [kSlots], then [kSlots] empty
+  kBarCount = kBarKVFull + 24
 };
-static_assert(kBarCount * 8 <= 256, "barriers fit");
+static_assert(kBarCount * 8 <= 400, "barriers fit");
 
 struct Shared {  // at Geom::kMisc
   uint32_t tmem;
@@ -195,11 +212,6 @@ struct Shared {  // at Geom::kMisc
   int odd_v[2];   // per unit slot: V values of an edge tile were left out
   Unit unit[2];
 };
-
-// mbar_wait by a whole warp, with one answer for its lanes
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  return __all_sync(kFull, mbar_wait(bar, parity, stop));
-}
 
 // A running position in a ring of barriers
 struct Ring {
@@ -214,9 +226,10 @@ struct Ring {
 };
 
 // The key tiles of a unit's query tile q: tokens [i0 + q W1, ...) of n
-__device__ __forceinline__ int key_tiles(int i0, int q, int W1, int n, int keys) {
+template <int KT>
+__device__ __forceinline__ int key_tiles(int i0, int q, int W1, int n) {
   const int first = i0 + q * W1;
-  return first < n ? (min(n, first + W1) + keys - 1) / keys : 0;
+  return first < n ? (min(n, first + W1) + KT - 1) / KT : 0;
 }
 
 template <int D, bool MASS>
@@ -225,11 +238,11 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
                                                                       const __grid_constant__ CUtensorMap mv,
                                                                       const __grid_constant__ PromptDev pd) {
   using Geo = Geom<D>;
-  constexpr int QT = Geo::kQT, KT = Geo::kKeys, NS = Geo::kSlots;
+  constexpr int QT = Geo::kQT, NS = Geo::kSlots, KT = Geo::kKeys, NB = Geo::kNB;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const PromptArgs& a = pd.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);  // uniform
   const int G = a.cfg.group_size, nh = a.cfg.num_kv_heads;
   const int W1 = pd.tile_tokens;  // query tokens per query tile
   const uint32_t s0 = smem_u32(smem), bars = s0 + Geo::kBar;
@@ -244,9 +257,12 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
   if (tid == 0) {
     mbar_init(bar(kBarQFull), 1);
     mbar_init(bar(kBarQEmpty), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar(kBarS + i), 1);
       mbar_init(bar(kBarP + i), 4);
+      mbar_init(bar(kBarH + i), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarO + i), 1);
       mbar_init(bar(kBarUFull + i), 1);
       mbar_init(bar(kBarUEmpty + i), 4 * QT + 3);
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
   const uint32_t tm = sh->tmem;
 
   if (warp >= 4 * QT) {
-    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KVQ_RD));
     const int role = warp - 4 * QT;
     if (role == 3) {
       // ------------------------------------------------------------ units
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
           if (u.n < 0) break;
           const int i0 = u.run * W1 * QT;
           int nk = 0;
-          for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles(i0, q, W1, u.n, KT));
+          for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles<KT>(i0, q, W1, u.n));
           if (!(ok = mbar_wait(bar(kBarQEmpty), ph_q ^ 1u, stop))) break;
           ph_q ^= 1u;
           mbar_expect_tx(bar(kBarQFull), QT * W1 * G * D * 2);
@@ -323,14 +339,20 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             for (int c = 0; c < D / 64; ++c)
               tma_load(s0 + Geo::kQ + q * Geo::kQTile + c * kRows * 128, &mq, 64 * c, u.head * G,
                        u.first + i0 + q * W1, bar(kBarQFull));
-          for (int t = 0; t < 2 * nk && ok; ++t) {
-            if (!(ok = mbar_wait(bar(kBarKVFull + NS + kv.slot), kv.phase ^ 1u, stop))) break;
+          // in the order the MMA warp takes them: K0 .. K(NB-1) V0 K(NB) V1 ...
+          auto load = [&](const CUtensorMap* map, int j) {
+            if (!ok || j >= nk || !(ok = mbar_wait(bar(kBarKVFull + NS + kv.slot), kv.phase ^ 1u, stop))) return;
             mbar_expect_tx(bar(kBarKVFull + kv.slot), Geo::kSlot);
             for (int c = 0; c < D / 64; ++c)
-              tma_load(s0 + Geo::kKV + kv.slot * Geo::kSlot + c * KT * 128, (t & 1) ? &mv : &mk, 64 * c, u.head,
-                       u.first + (t >> 1) * KT, bar(kBarKVFull + kv.slot));
+              tma_load(s0 + Geo::kKV + kv.slot * Geo::kSlot + c * KT * 128, map, 64 * c, u.head, u.first + j * KT,
+                       bar(kBarKVFull + kv.slot));
             kv.next(NS);
             issued = min(issued + 1, NS);
+          };
+          for (int j = 0; j < NB; ++j) load(&mk, j);
+          for (int j = 0; j < nk && ok; ++j) {
+            load(&mv, j);
+            load(&mk, j + NB);
           }
         }
         if (*stop) {  // copies in flight land before the shared memory is given back
@@ -347,107 +369,112 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
       }
     } else if (role == 0) {
       // ------------------------------------------------------------ matrix instructions
-      if (lane == 0) {
-        Ring ru, kv;
-        uint32_t ph_q = 0, ph_p[2] = {0u, 0u}, ph_v = 0;
-        bool ok = true;
-        // S[buf] = Q_q K^T with K in slot `slot`
-        auto score = [&](int q, int buf, int slot) {
-          const uint32_t qa = s0 + Geo::kQ + q * Geo::kQTile, ka = s0 + Geo::kKV + slot * Geo::kSlot;
+      // The whole warp runs this, on values it knows to be uniform, and one
+      // elected lane issues: descriptors then stay in uniform registers (from
+      // a single-lane branch each instruction took about 70 cycles to issue).
+      Ring ru, kv;
+      uint32_t ph_q = 0, ph_p = 0, ph_v = 0;  // ph_p: a bit per P buffer
+      bool ok = true;
+      const bool leader = elect_one();
+      const uint64_t dq = sw128_desc(s0 + Geo::kQ, 0), dk = sw128_desc(s0 + Geo::kKV, 0);
+      const uint64_t dv = sw128_desc(s0 + Geo::kKV, KT * 128);
+      auto commit = [&](int b) {
+        if (leader) mma_commit(bar(b));
+      };
+      // score tile j of query tile q: S = Q_q K^T with K in slot `slot`
+      auto score = [&](int q, int j, int slot) {
+        const int b = 2 * q + j % NB;
+        const uint64_t qa = dq + (q * Geo::kQTile >> 4), ka = dk + (slot * Geo::kSlot >> 4);
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tm + Geo::kS + buf * KT, sw128_desc(qa + (k >> 2) * kRows * 128 + (k & 3) * 32, 0),
-                   sw128_desc(ka + (k >> 2) * KT * 128 + (k & 3) * 32, 0), idesc_m128(KT, false), k != 0);
-          mma_commit(bar(kBarS + buf));
-        };
-        // O_q (+)= P[buf] V with V in slot `slot`
-        auto value = [&](int q, int buf, int slot, bool acc) {
-          const uint32_t va = s0 + Geo::kKV + slot * Geo::kSlot;
+            mma_ss(tm + Geo::kS + (NB * q + j % NB) * KT, qa + (((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
+                   ka + (((k >> 2) * KT * 128 + (k & 3) * 32) >> 4), idesc_m128(KT, false), k != 0);
+          mma_commit(bar(kBarS + b));
+        }
+      };
+      // O_q (+)= P V with V in slot `slot`, half h of the keys
+      auto value = [&](int q, int j, int slot, int h) {
+        const uint64_t va = dv + (slot * Geo::kSlot >> 4);
+        if (leader) {
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            mma_ts(tm + Geo::kO + q * D, tm + Geo::kS + buf * KT + 8 * k, sw128_desc(va + k * 2048, KT * 128),
-                   idesc_m128(D, true), acc || k > 0);
-          mma_commit(bar(kBarO + q));
-        };
-        auto wait_kv = [&] {
-          const bool r = mbar_wait(bar(kBarKVFull + kv.slot), kv.phase, stop);
-          fence_after();
-          return r;
-        };
-        auto wait_p = [&](int buf) {
-          const bool r = mbar_wait(bar(kBarP + buf), ph_p[buf], stop);
-          ph_p[buf] ^= 1u;
-          fence_after();
-          return r;
-        };
-        while (ok) {
-          if (!mbar_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
-          const Unit u = sh->unit[ru.slot];
-          mbar_arrive(bar(kBarUEmpty + ru.slot));
-          ru.next(2);
-          if (u.n < 0) break;
-          const int i0 = u.run * W1 * QT, edge = i0 / KT;
-          int nkq[2] = {key_tiles(i0, 0, W1, u.n, KT), QT == 2 ? key_tiles(i0, 1, W1, u.n, KT) : 0};
-          const int nk = max(nkq[0], nkq[1]);
-          if (!(ok = mbar_wait(bar(kBarQFull), ph_q, stop))) break;
-          ph_q ^= 1u;
-          if (!(ok = wait_kv())) break;  // K of tile 0
-          score(0, 0, kv.slot);
-          if (QT == 2 && nkq[1] > 0) score(1, 1, kv.slot);
-          mma_commit(bar(kBarKVFull + NS + kv.slot));
-          if (nk == 1) mma_commit(bar(kBarQEmpty));
+          for (int k = h * KT / 32; k < (h + 1) * KT / 32; ++k)
+            mma_ts(tm + Geo::kO + q * D, tm + Geo::kS + (NB * q + j % NB) * KT + 8 * k, va + (k * 2048 >> 4), idesc_m128(D, true),
+                   j > 0 || k > 0);
+          if (h == 1) mma_commit(bar(kBarO + q + j % NB));
+        }
+      };
+      auto wait_kv = [&] {
+        const bool r = warp_wait(bar(kBarKVFull + kv.slot), kv.phase, stop);
+        fence_after();
+        return r;
+      };
+      while (ok) {
+        if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
+        const int n = __shfl_sync(kFull, sh->unit[ru.slot].n, 0);
+        const int i0 = __shfl_sync(kFull, sh->unit[ru.slot].run, 0) * W1 * QT, edge = i0 / KT;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarUEmpty + ru.slot));
+        ru.next(2);
+        if (n < 0) break;
+        const int nkq[2] = {key_tiles<KT>(i0, 0, W1, n), QT == 2 ? key_tiles<KT>(i0, 1, W1, n) : 0};
+        const int nk = max(nkq[0], nkq[1]);
+        if (!(ok = warp_wait(bar(kBarQFull), ph_q, stop))) break;
+        ph_q ^= 1u;
+        // the first NB score tiles; later ones follow the PV that frees their buffer
+        for (int j = 0; j < min(nk, NB); ++j) {
+          if (!(ok = wait_kv())) break;
+#pragma unroll
+          for (int q = 0; q < QT; ++q)
+            if (j < nkq[q]) score(q, j, kv.slot);
+          commit(kBarKVFull + NS + kv.slot);
           kv.next(NS);
-          for (int j = 0; j < nk && ok; ++j) {
-            const Ring v = kv;
-            Ring k2 = kv;  // K of tile j + 1
-            k2.next(NS);
-            if (!(ok = wait_kv())) break;
-            bool guarded = j >= edge;  // the guard looks at V while the softmax of the tile runs
-            if (guarded) mbar_arrive(bar(kBarG));
-            auto wait_guard = [&] {
-              if (!guarded) return true;
-              guarded = false;
-              const bool r = mbar_wait(bar(kBarV), ph_v, stop);
-              ph_v ^= 1u;
-              fence_after();
-              return r;
-            };
-            kv.next(NS);
-            if constexpr (QT == 2) {
-              bool have_k = false;
+        }
+        if (!ok) break;
+        if (nk <= NB) commit(kBarQEmpty);
+        for (int j = 0; j < nk; ++j) {
+          const int vslot = kv.slot;
+          if (!(ok = wait_kv())) break;
+          kv.next(NS);
+          bool guarded = j >= edge;  // the guard looks at V while the softmax of the tile runs
+          if (guarded && lane == 0) mbar_arrive(bar(kBarG));
+          bool have_k = false;
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                if (j >= nkq[q]) continue;
-                if (!(ok = wait_p(q) && wait_guard())) break;
-                value(q, q, v.slot, j > 0);
-                if (j + 1 < nkq[q]) {
-                  if (!have_k && !(ok = wait_kv())) break;
-                  have_k = true;
-                  score(q, q, k2.slot);
-                }
-              }
-            } else {
-              if (j + 1 < nk) {
-                if (!(ok = wait_kv())) break;
-                score(0, (j + 1) & 1, k2.slot);
-              }
-              if (!(ok = wait_p(j & 1) && wait_guard())) break;
-              value(0, j & 1, v.slot, j > 0);
+          for (int q = 0; q < QT; ++q) {
+            if (!ok || j >= nkq[q]) continue;
+            const int b = 2 * q + j % NB;
+            ok = warp_wait(bar(kBarH + b), (ph_p >> b) & 1u, stop);
+            if (ok && guarded) {
+              ok = warp_wait(bar(kBarV), ph_v, stop);
+              ph_v ^= 1u;
+              guarded = false;
             }
-            if (!ok) break;
-            mma_commit(bar(kBarKVFull + NS + v.slot));
-            if (j + 1 < nk) {
-              mma_commit(bar(kBarKVFull + NS + k2.slot));
-              if (j + 2 == nk) mma_commit(bar(kBarQEmpty));
-              kv.next(NS);
+            fence_after();
+            if (!ok) continue;
+            value(q, j, vslot, 0);
+            if (!(ok = warp_wait(bar(kBarP + b), (ph_p >> b) & 1u, stop))) continue;
+            ph_p ^= 1u << b;
+            fence_after();
+            value(q, j, vslot, 1);
+            if (j + NB < nkq[q]) {
+              if (!have_k && !(ok = wait_kv())) continue;
+              have_k = true;
+              score(q, j + NB, kv.slot);
             }
+          }
+          if (!ok) break;
+          commit(kBarKVFull + NS + vslot);
+          if (j + NB < nk) {
+            commit(kBarKVFull + NS + kv.slot);
+            if (j + NB + 1 == nk) commit(kBarQEmpty);
+            kv.next(NS);
           }
         }
-        if (*stop) {  // matrix instructions in flight end before TMEM is freed
-          mma_commit(bar(kBarDrain));
-          const long long t0 = global_ns();
-          while (!mbar_try(bar(kBarDrain), 0) && global_ns() - t0 < kWaitLimitNs) {
-          }
+      }
+      if (*stop && leader) {  // matrix instructions in flight end before TMEM is freed
+        mma_commit(bar(kBarDrain));
+        const long long t0 = global_ns();
+        while (!mbar_try(bar(kBarDrain), 0) && global_ns() - t0 < kWaitLimitNs) {
         }
       }
     } else {
@@ -463,10 +490,10 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
         if (u.n < 0) break;
         const int i0 = u.run * W1 * QT, edge = i0 / KT;
         int nk = 0;
-        for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles(i0, q, W1, u.n, KT));
+        for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles<KT>(i0, q, W1, u.n));
         bool ok = true;
+        for (int j = 0; j < min(nk, NB); ++j) kv.next(NS);  // K
         for (int j = 0; j < nk; ++j) {
-          kv.next(NS);  // K
           if (j >= edge) {
             if (!(ok = warp_wait(bar(kBarG), ph_g, stop))) break;
             ph_g ^= 1u;
@@ -497,7 +524,8 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarV));
           }
-          kv.next(NS);  // V
+          kv.next(NS);                   // V
+          if (j + NB < nk) kv.next(NS);  // K
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
@@ -505,7 +533,7 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
     }
   } else {
     // -------------------------------------------------------------- softmax
-    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KVQ_RI));
     const int q = warp >> 2, row = tid & 127;
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tm + Geo::kO + q * D + tlane;
@@ -513,7 +541,9 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
     float* s_m = reinterpret_cast<float*>(smem + Geo::kStat) + q * 2 * kRows;
     float* s_w = s_m + kRows;
     Ring ru;
-    uint32_t ph_s[2] = {0u, 0u}, ph_o = 0;
+    uint32_t ph_s[2] = {0u, 0u}, ph_o[2] = {0u, 0u};
+    const bool leader = elect_one();
+    constexpr int HK = KT / 2;  // keys of half a tile
     while (true) {
       if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
       const Unit u = sh->unit[ru.slot];
@@ -521,7 +551,7 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
       ru.next(2);
       if (u.n < 0) break;
       const int first = u.run * W1 * QT + q * W1;        // the tile's first token
-      const int nk = key_tiles(first, 0, W1, u.n, KT);
+      const int nk = key_tiles<KT>(first, 0, W1, u.n);
       const int ti = first + row / G;                    // this row's token
       const bool live = row < W1 * G && ti < u.n;
       const int vis = live ? ti : u.n - 1;               // last key this row sees
@@ -531,82 +561,106 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nk; ++j) {
-        const int buf = QT == 2 ? q : j & 1;
-        const uint32_t tS = tm + Geo::kS + buf * KT + tlane;
-        if (!(ok = warp_wait(bar(kBarS + buf), ph_s[buf], stop))) break;
+        const int buf = j % NB;
+        const uint32_t tS = tm + Geo::kS + (NB * q + buf) * KT + tlane;
+        if (!(ok = warp_wait(bar(kBarS + 2 * q + buf), ph_s[buf], stop))) break;
         ph_s[buf] ^= 1u;
         fence_after();
+        // The tile goes in two halves.  The first half's weights are taken
+        // relative to the maximum up to it while the second half's scores are
+        // still on their way and being compared; P V starts on them while the
+        // second half's weights are computed.
         float s[KT];
-        tmem_ld32<0>(tS, s);
-        tmem_ld32<32>(tS + 32, s);
-        if constexpr (KT == 128) {
-          tmem_ld32<KT - 64>(tS + 64, s);
-          tmem_ld32<KT - 32>(tS + 96, s);
-        }
-        tmem_wait32<0>(s);
-        tmem_wait32<32>(s);
-        if constexpr (KT == 128) {
-          tmem_wait32<KT - 64>(s);
-          tmem_wait32<KT - 32>(s);
-        }
-        if (j >= masked) {
-          const int lim = vis - j * KT;
+        const int lim = vis - j * KT;  // last key of the tile that the row sees
+        // loads of half h, its mask and maximum (times the scale)
+        auto load = [&](auto at) {
+          constexpr int o = decltype(at)::value;
+          tmem_ld32<o>(tS + o, s);
+          if constexpr (HK == 64) tmem_ld32<o + HK - 32>(tS + o + 32, s);
+        };
+        auto top_of = [&](auto at) {
+          constexpr int o = decltype(at)::value;
+          tmem_wait32<o>(s);
+          if constexpr (HK == 64) tmem_wait32<o + HK - 32>(s);
+          if (j >= masked) {
 #pragma unroll
-          for (int c = 0; c < KT; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < KT; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = c + 4 + e < KT ? max3f(mx[e], s[c + e], s[c + 4 + e]) : fmaxf(mx[e], s[c + e]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * pd.qscale;
-        const bool grow = top > m + kLazy;  // (m = -inf before the first finite score)
-        float alpha = 1.f;
-        if (grow) {
-          alpha = ex2(m - top);
-          m = top;
-          l *= alpha;
-        }
-        if (j > 0 && __any_sync(kFull, grow)) {
-          if constexpr (QT == 1) {  // (with two query tiles this score tile's MMA came after that PV)
-            if (!(ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop))) break;
-            fence_after();
+            for (int c = o; c < o + HK; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
           }
+          float mx[4] = {s[o], s[o + 1], s[o + 2], s[o + 3]};
+#pragma unroll
+          for (int c = o + 4; c < o + HK - 4; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = max3nan(mx[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3nan(mx[e], s[o + HK - 4 + e], s[o + HK - 4 + e]);
+          const float t = max3nan(mx[0], mx[1], max3nan(mx[2], mx[3], mx[3])) * pd.qscale;
+          if (!(t < INFINITY)) l = NAN;  // a NaN or an infinite score: the row is NaN
+          return t;
+        };
+        // The maximum moves to `top` in the lanes where it is more than kLazy
+        // larger (m = -inf before the first finite score); O and l follow.
+        auto grow = [&](float top) {
+          float alpha = 1.f;
+          if (top > m + kLazy) {
+            alpha = ex2(m - top);
+            m = top;
+            l *= alpha;
+          }
+          if (j == 0) return true;
+          // the last PV is done: with one score buffer this tile's score MMA came after it
+          if (NB > 1 && !warp_wait(bar(kBarO + q + (j - 1) % NB), ph_o[(j - 1) % NB] ^ 1u, stop)) return false;
+          fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32<0>(tO + c, o);
-            tmem_wait32<0>(o);
-            uint32_t x[32];
+          for (int c = 0; c < D; c += 8) {  // few registers: the scores stay in theirs
+            float o[8];
+            tmem_ld8(tO + c, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * alpha);
-            tmem_st32<0>(tO + c, x);
+            for (int e = 0; e < 8; ++e) o[e] *= alpha;
+            tmem_st8(tO + c, o);
           }
-        }
-        const float mu = m == -INFINITY ? 0.f : m;  // a row with no finite score so far
-        const float2 sc2 = make_float2(pd.qscale, pd.qscale), mu2 = make_float2(-mu, -mu);
+          return true;
+        };
         float2 part[KT / 32];  // sums of 32 keys
+        uint32_t p[HK / 2];
+        auto weigh = [&](auto at) {
+          constexpr int o = decltype(at)::value;
+          const float mu = m == -INFINITY ? 0.f : m;  // a row with no finite score so far
+          const float2 sc2 = make_float2(pd.qscale, pd.qscale), mu2 = make_float2(-mu, -mu);
 #pragma unroll
-        for (int h = 0; h < KT / 64; ++h) {
-          uint32_t p[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float2 x = __ffma2_rn(make_float2(s[64 * h + c], s[64 * h + c + 1]), sc2, mu2);
+          for (int c = 0; c < HK; c += 2) {
+            const float2 x = __ffma2_rn(make_float2(s[o + c], s[o + c + 1]), sc2, mu2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
-            float2& sum = part[2 * h + c / 32];
+            float2& sum = part[(o + c) / 32];
             sum = c % 32 == 0 ? e : __fadd2_rn(sum, e);
             p[c / 2] = h2_as_u32(__float22half2_rn(e));
           }
-          tmem_st32<0>(tS + 32 * h, p);
+        };
+        // P of 32 keys takes 16 columns of scores already read
+        auto store = [&](int o) {
+          if constexpr (HK == 64) tmem_st32<0>(tS + o / 2, p); else tmem_st16(tS + o / 2, p);
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+        };
+        constexpr std::integral_constant<int, 0> kFirst{};
+        constexpr std::integral_constant<int, HK> kSecond{};
+        load(kFirst);
+        float top = top_of(kFirst);
+        load(kSecond);
+        if (__any_sync(kFull, top > m + kLazy) && !(ok = grow(top))) break;
+        weigh(kFirst);
+        top = top_of(kSecond);
+        if (__any_sync(kFull, top > m + kLazy)) {  // rare: the first half again
+          if (!(ok = grow(top))) break;
+          weigh(kFirst);
         }
-        tmem_wait_st();
-        fence_before();
-        if constexpr (QT == 1) {  // one PV outstanding at most, so that a phase of kBarO is never passed over
-          if (j > 0 && !(ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop))) break;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + buf));
-        ph_o ^= 1u;
+        store(0);
+        mbar_arrive_if(leader, bar(kBarH + 2 * q + buf));
+        weigh(kSecond);
+        store(HK);
+        mbar_arrive_if(leader, bar(kBarP + 2 * q + buf));
+        ph_o[j % NB] ^= 1u;
+        const float mu = m == -INFINITY ? 0.f : m;
         float ps[KT / 32];
         float all = 0.f;
 #pragma unroll
@@ -629,7 +683,7 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
       if (!ok) break;
       if (nk > 0) {
         // ---- the tile's rows
-        if (!warp_wait(bar(kBarO + q), ph_o ^ 1u, stop)) break;
+        if (!warp_wait(bar(kBarO + q + (nk - 1) % NB), ph_o[(nk - 1) % NB] ^ 1u, stop)) break;
         fence_after();
         const bool odd = *static_cast<volatile int*>(&sh->odd_v[uslot]) != 0;
         const float inv = 1.f / l;
@@ -706,27 +760,27 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
 // tile t.  A CTA per 32 tiles: lanes over the tiles, warps over the (run,
 // head) rows with a fixed stride, then the warps in order.
 constexpr int kMassWarps = 32;
-__global__ void __launch_bounds__(kMassWarps * 32) prompt_mass_kernel(PromptDev pd, int keys) {
+__global__ void __launch_bounds__(kMassWarps * 32) prompt_mass_kernel(PromptDev pd, int KT) {
   __shared__ float s_sum[kMassWarps][33];
   const PromptArgs& a = pd.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s = blockIdx.y, t = blockIdx.x * 32 + lane;
   const int T = a.cfg.tile_tokens, W1 = pd.tile_tokens, nh = a.cfg.num_kv_heads;
-  const int wid = min(T, keys), per = T / wid;  // partial sums per tile of T
+  const int wid = min(T, KT), per = T / wid;  // partial sums per tile of T
   Unit u{s, 0, 0, 0, 0};
   u.n = seq_len(a, s, u.first);
   const int tiles = min((u.n + T - 1) / T, a.max_tiles);
   if (blockIdx.x * 32 >= tiles) return;
   const int w0 = a.mass_window == 0 ? 0 : max(0, u.n - a.mass_window) / W1;
   const int r0 = max(w0, blockIdx.x * 32 * T / W1), rows = (u.n + W1 - 1) / W1 * nh;
-  const size_t stride = static_cast<size_t>(pd.max_tiles_k) * (keys / wid);
+  const size_t stride = static_cast<size_t>(pd.max_tiles_k) * (KT / wid);
   float sum = 0.f;
 #pragma unroll 4
   for (int x = r0 * nh + warp; x < rows; x += kMassWarps) {
     u.head = x % nh;
     const int run = x / nh;
     // the key tiles this query tile went over
-    const int held = (min(u.n, (run + 1) * W1) + keys - 1) / keys * (keys / wid);
+    const int held = (min(u.n, (run + 1) * W1) + KT - 1) / KT * (KT / wid);
     const float* p = pd.part + static_cast<size_t>(mass_slot(pd, u, run)) * stride;
     for (int k = 0; k < per; ++k)
       if (t < tiles && t * per + k < held) sum += p[t * per + k];
@@ -767,10 +821,9 @@ bool make_map(CUtensorMap* m, const void* base, int d, int heads, int tokens, lo
 }
 
 int tile_tokens(const kvq_config& cfg) { return kRows / cfg.group_size; }
-int query_tiles(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kQT : Geom<128>::kQT; }
 int key_tile(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kKeys : Geom<128>::kKeys; }
-static_assert(Geom<64>::kQT == Geom<128>::kQT && Geom<64>::kKeys == Geom<128>::kKeys, "shapes of d = 64");
-
+static_assert(Geom<64>::kKeys == Geom<128>::kKeys, "key tiles of d = 64");
+int query_tiles(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kQT : Geom<128>::kQT; }
 struct PromptSizes {
   long long units;
   int max_tiles_k, window_runs, grid;

@@ -17,6 +17,13 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// true in one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
+
 // ---- mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -45,6 +52,14 @@ __device__ __forceinline__ long long global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// arrive from the lane where `who` is set, without a branch
+__device__ __forceinline__ void mbar_arrive_if(bool who, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n @p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}" ::"r"(
+          bar),
+      "r"(static_cast<uint32_t>(who))
+      : "memory");
+}
 // Wait for a phase; false once the limit passes or `stop` (shared memory, set
 // by whichever warp of the CTA gave up first) is set.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
@@ -58,6 +73,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
   }
   return true;
+}
+
+// The same by a whole warp, with one answer for its lanes (the common case is
+// one try and one vote).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  if (__all_sync(kFull, mbar_try(bar, parity))) return true;
+  return __all_sync(kFull, mbar_wait(bar, parity, stop));
 }
 
 // ---- TMA: one box of a 3-D map (channel, head, row)
@@ -152,6 +174,19 @@ template <int O, int N>
 __device__ __forceinline__ void tmem_wait32(float (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_W32(v, O));
 }
+// eight columns, loaded and waited for
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 #undef KVQ_R32
 #undef KVQ_W32
 template <int O, int N>
@@ -165,6 +200,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&v)[N])
       "r"(v[O + 14]), "r"(v[O + 15]), "r"(v[O + 16]), "r"(v[O + 17]), "r"(v[O + 18]), "r"(v[O + 19]),
       "r"(v[O + 20]), "r"(v[O + 21]), "r"(v[O + 22]), "r"(v[O + 23]), "r"(v[O + 24]), "r"(v[O + 25]),
       "r"(v[O + 26]), "r"(v[O + 27]), "r"(v[O + 28]), "r"(v[O + 29]), "r"(v[O + 30]), "r"(v[O + 31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
