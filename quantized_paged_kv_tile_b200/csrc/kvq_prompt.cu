@@ -45,9 +45,12 @@ using namespace sm100;
 
 constexpr int kRows = 128;    // query rows per query tile (TMEM lanes)
 // The running maximum a row's weights are relative to follows the true one
-// only once that is more than 2^kLazy larger: weights reach 2^8 then (fp16 and
-// the fp32 sums hold that as exactly as 1), and O is rescaled rarely.
-constexpr float kLazy = 8.f;
+// only once that is more than kLazy larger (log2 units): weights reach 2^15
+// then, below fp16's 65504 and held by it and the fp32 sums as exactly as 1.
+// A rescale of O costs a warp about as much as a tile's exponentials; with
+// keys of very different channel stds (scores spread over some 30 units) a
+// limit of 8 took 4853 us on 16384 tokens x 64 heads.
+constexpr float kLazy = 15.f;
 // up to this many sequences the units are taken longest first
 constexpr int kSortedSeqs = 1024;
 
@@ -147,8 +150,6 @@ __device__ __forceinline__ long long mass_slot(const PromptDev& pd, const Unit& 
   return (static_cast<long long>(u.seq) * pd.window_runs + (run - r0)) * a.cfg.num_kv_heads + u.head;
 }
 
-__device__ __forceinline__ float max3f(float x, float y, float z) { return fmaxf(fmaxf(x, y), z); }
-
 // max that keeps NaN
 __device__ __forceinline__ float max3nan(float x, float y, float z) {
   float r;
@@ -156,62 +157,71 @@ __device__ __forceinline__ float max3nan(float x, float y, float z) {
   return r;
 }
 
-#ifndef KVQ_RD
-#define KVQ_RD 88
-#define KVQ_RI 208
-#endif
-#ifndef KVQ_KT
-#define KVQ_KT 128
-#endif
 // Shapes per head size.  kQT query tiles of 128 rows share the key tiles that
-// the CTA loads, one softmax warpgroup each; TMEM holds two score tiles and
-// one output tile per query tile.
-template <int D>
+// the CTA loads.  Each has its own softmax warpgroup, its own warp that issues
+// its matrix instructions, and its own score, P and output tiles in TMEM.
+// At d = 64 and 256 P has columns of its own, so the next scores can be
+// computed as soon as the softmax has read the last ones.  At d = 128 the two
+// output tiles leave no room for that: P lies over S.
+template <int D, bool MASS>
 struct Geom {
   static constexpr int kQT = D == 256 ? 1 : 2;
-  static constexpr int kKeys = D == 256 ? 64 : KVQ_KT;   // keys per tile
-  static constexpr int kNB = kKeys == 64 ? 2 : 1;        // score tiles per query tile in TMEM
-  static constexpr int kSlot = kKeys * D * 2;            // one K or V tile
-  static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 8 * 64 / kKeys : 8);
-  static constexpr int kSoftmax = kQT * 128;             // softmax threads
-  static constexpr int kThreads = kSoftmax + 128;        // + MMA, load, V guard and unit warps
+  static constexpr bool kOver = D == 128;               // P over S
+  static constexpr int kKeys = D == 256 ? 64 : 128;     // keys per tile
+  // With P over S a query tile waits for its MMAs between P and the next
+  // scores: the two softmaxes take turns at the exponentials, so that one's
+  // MMAs run under the other's exponentials (left alone they drift into step:
+  // 1171 against 1218 TFLOP/s).  Where nothing waits, turns only cost (d = 64:
+  // 608 against 654).
+  static constexpr bool kTurns = kOver;
+  static constexpr int kSlot = kKeys * D * 2;                                  // one K or V tile
+  static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 4 : 8);
+  static constexpr int kThreads = kQT * 128 + 128;      // softmax; two MMA warps, loads, V guard and units
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kQ = 0;
   static constexpr int kKV = kQ + kQT * kQTile;
-  static constexpr int kStat = kKV + kSlots * kSlot;     // float m[128], w[128] per query tile (masses)
+  static constexpr int kStat = kKV + kSlots * kSlot;    // float m[128], w[128] per query tile (masses)
   static constexpr int kBar = kStat + kQT * 2 * kRows * 4;
-  static constexpr int kMisc = kBar + 400;
-  static constexpr int kSmem = kMisc + 128 + 1024;       // + alignment slack
+  static constexpr int kMisc = kBar + 384;
+  static constexpr int kSmem = kMisc + 128 + 1024;      // + alignment slack
   static_assert(kSmem <= 232448, "shared memory per block");
-  // TMEM columns
-  static constexpr int kS = 0, kO = kNB * kQT * kKeys;
-  static_assert(kO + kQT * D <= 512, "TMEM columns");
+  // TMEM columns: S and P of query tile q from q * kTile on, O after them
+  static constexpr int kTile = D == 64 ? 192 : 128;
+  static constexpr int kO = kQT * kTile;
+  static constexpr int kP = kOver ? 0 : kKeys;
+  static_assert((kOver ? kKeys : kKeys + kKeys / 2) <= kTile && kO + kQT * D <= 512, "TMEM columns");
 };
 
-// mbarriers, 8 bytes each, from Geom::kBar on
+// mbarriers, 8 bytes each, from Geom::kBar on; [q]: one per query tile
+constexpr int kUnitSlots = 4;
 enum : int {
-  kBarQFull = 0,         // the unit's Q tiles have landed
-  kBarQEmpty,            // its last score MMA has read them
-  kBarS,                 // [2 x query tile + buffer] a score tile is in TMEM
-  kBarP = kBarS + 4,     // [same] its P is in TMEM (one arrival per softmax warp)
-  kBarH = kBarP + 4,     // [same] the first half of its P is
-  kBarO = kBarH + 4,     // [query tile + buffer] a PV MMA is done
-  kBarG = kBarO + 2,     // V of an edge tile has landed: the guard may look at it
-  kBarV,                 // the guard is done with it
-  kBarUFull,             // [2] a unit is published
-  kBarUEmpty = kBarUFull + 2,  // [2] every warp is done with it
-  kBarDrain = kBarUEmpty + 2,
-  kBarKVFull,            // [kSlots], then [kSlots] empty
-  kBarCount = kBarKVFull + 24
+  kBarQFull = 0,             // the unit's Q tiles have landed
+  kBarQEmpty,                // the last score MMAs have read them
+  kBarS,                     // [q] a score tile is in TMEM
+  kBarF = kBarS + 2,         // [q] the softmax has read it (one arrival per warp)
+  kBarH = kBarF + 2,         // [q] the first half of its P is in TMEM (one arrival per warp)
+  kBarI = kBarH + 2,         // [q] three quarters are
+  kBarP = kBarI + 2,         // [q] all of it is
+  kBarO = kBarP + 2,         // [q] its P V is done
+  kBarT = kBarO + 2,         // [q] query tile q's turn at the exponentials
+  kBarG = kBarT + 2,         // V of an edge tile has landed: the guard may look at it
+  kBarV,                     // the guard is done with it
+  kBarUFull,                 // [unit slot] a unit is published
+  kBarUEmpty = kBarUFull + kUnitSlots,  // [unit slot] every warp is done with it
+  kBarDrain = kBarUEmpty + kUnitSlots,  // [q]
+  kBarKVFull = kBarDrain + 2,           // [slot] a K or V tile has landed
+  kBarKVEmpty = kBarKVFull + 8,         // [slot] every MMA that reads it is done
+  kBarCount = kBarKVEmpty + 8
 };
-static_assert(kBarCount * 8 <= 400, "barriers fit");
+static_assert(kBarCount * 8 <= 384, "barriers fit");
 
 struct Shared {  // at Geom::kMisc
   uint32_t tmem;
   int stop;
-  int odd_v[2];   // per unit slot: V values of an edge tile were left out
-  Unit unit[2];
+  int odd_v[kUnitSlots];  // per unit: V values of an edge tile were left out
+  Unit unit[kUnitSlots];
 };
+static_assert(sizeof(Shared) <= 128, "shared words fit");
 
 // A running position in a ring of barriers
 struct Ring {
@@ -233,12 +243,12 @@ __device__ __forceinline__ int key_tiles(int i0, int q, int W1, int n) {
 }
 
 template <int D, bool MASS>
-__global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap mq,
-                                                                      const __grid_constant__ CUtensorMap mk,
-                                                                      const __grid_constant__ CUtensorMap mv,
-                                                                      const __grid_constant__ PromptDev pd) {
-  using Geo = Geom<D>;
-  constexpr int QT = Geo::kQT, NS = Geo::kSlots, KT = Geo::kKeys, NB = Geo::kNB;
+__global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap mq,
+                                                                            const __grid_constant__ CUtensorMap mk,
+                                                                            const __grid_constant__ CUtensorMap mv,
+                                                                            const __grid_constant__ PromptDev pd) {
+  using Geo = Geom<D, MASS>;
+  constexpr int QT = Geo::kQT, NS = Geo::kSlots, KT = Geo::kKeys, NU = kUnitSlots;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const PromptArgs& a = pd.a;
@@ -251,28 +261,33 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
   volatile int* stop = &sh->stop;
 
   // rows of the Q tiles that no box fills (g not a divisor of 128) stay zero
-  for (int i = tid; i < QT * Geo::kQTile / 16; i += Geo::kThreads)
-    reinterpret_cast<uint4*>(smem + Geo::kQ)[i] = make_uint4(0, 0, 0, 0);
-  fence_async_smem();
+  if (kRows % G != 0) {
+    for (int i = tid; i < QT * Geo::kQTile / 16; i += Geo::kThreads)
+      reinterpret_cast<uint4*>(smem + Geo::kQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_async_smem();
+  }
   if (tid == 0) {
     mbar_init(bar(kBarQFull), 1);
-    mbar_init(bar(kBarQEmpty), 1);
-    for (int i = 0; i < 4; ++i) {
+    mbar_init(bar(kBarQEmpty), QT);
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarS + i), 1);
+      mbar_init(bar(kBarF + i), 4);
       mbar_init(bar(kBarP + i), 4);
       mbar_init(bar(kBarH + i), 4);
-    }
-    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBarI + i), 4);
+      mbar_init(bar(kBarT + i), 4);
       mbar_init(bar(kBarO + i), 1);
-      mbar_init(bar(kBarUFull + i), 1);
-      mbar_init(bar(kBarUEmpty + i), 4 * QT + 3);
+      mbar_init(bar(kBarDrain + i), 1);
     }
-    mbar_init(bar(kBarG), 1);
+    mbar_init(bar(kBarG), QT);
     mbar_init(bar(kBarV), 1);
-    mbar_init(bar(kBarDrain), 1);
+    for (int i = 0; i < NU; ++i) {
+      mbar_init(bar(kBarUFull + i), 1);
+      mbar_init(bar(kBarUEmpty + i), 4 * QT + QT + 2);
+    }
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(kBarKVFull + i), 1);
-      mbar_init(bar(kBarKVFull + NS + i), 1);
+      mbar_init(bar(kBarKVEmpty + i), QT);
     }
     mbar_init_fence();
     sh->stop = 0;
@@ -284,39 +299,121 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
   const uint32_t tm = sh->tmem;
 
   if (warp >= 4 * QT) {
-    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(KVQ_RD));
+    // (88 and 208 of the 168 registers a thread the block has at launch)
+    if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     const int role = warp - 4 * QT;
-    if (role == 3) {
-      // ------------------------------------------------------------ units
-      if (blockIdx.x == 0) {
-        for (int s = lane; s < a.num_seqs; s += 32) {
-          const int f = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-          if (f < 0 || e < f || e > a.total_tokens || e - f > a.max_seq_tokens)
-            report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
+    if (role < QT) {
+      // ------------------------------------------------------------ matrix instructions of query tile `role`
+      // The whole warp runs this, on values it knows to be uniform, and one
+      // elected lane issues: descriptors then stay in uniform registers (from
+      // a single-lane branch each instruction took about 70 cycles to issue).
+      const int q = role;
+      Ring ru, kv;
+      uint32_t ph_q = 0, ph_f = 0, ph_p = 0, ph_v = 0;
+      bool ok = true;
+      const bool leader = elect_one();
+      const uint32_t tS = tm + q * Geo::kTile, tP = tS + Geo::kP, tO = tm + Geo::kO + q * D;
+      const uint64_t dq = sw128_desc(s0 + Geo::kQ + q * Geo::kQTile, 0), dk = sw128_desc(s0 + Geo::kKV, 0);
+      const uint64_t dv = sw128_desc(s0 + Geo::kKV, KT * 128);
+      auto commit = [&](int b) {
+        if (leader) mma_commit(bar(b));
+      };
+      auto wait_kv = [&](const Ring& at) {
+        if (!ok) return;
+        ok = warp_wait(bar(kBarKVFull + at.slot), at.phase, stop);
+        fence_after();
+      };
+      // S = Q K^T with the K tile at hand
+      auto score = [&](const Ring& at) {
+        if constexpr (!Geo::kOver) {  // once the softmax has read the last S
+          if (!ok || !(ok = warp_wait(bar(kBarF + q), ph_f ^ 1u, stop))) return;
+          ph_f ^= 1u;
+          fence_after();
         }
-      }
-      Ring r;
-      for (int round = 0;; ++round) {
-        const long long ul = static_cast<long long>(round) * gridDim.x +
-                             ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        Unit u{0, 0, 0, -1, 0};  // n = -1: no more
-        if (ul < pd.units) {
-          u = locate_unit(pd, static_cast<int>(ul), lane);
-          if (u.n == 0) {
-            if (a.num_seqs > kSortedSeqs) continue;
-            u.n = -1;
+        const uint64_t ka = dk + (at.slot * Geo::kSlot >> 4);
+        if (leader && ok) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tS, dq + (((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
+                   ka + (((k >> 2) * KT * 128 + (k & 3) * 32) >> 4), idesc_m128(KT, false), k != 0);
+          mma_commit(bar(kBarS + q));
+        }
+      };
+      // O (+)= P V over the keys [16 k0, 16 k1) of tile j
+      auto value = [&](const Ring& at, int j, auto k0, auto k1) {
+        const uint64_t va = dv + (at.slot * Geo::kSlot >> 4);
+        fence_after();
+        if (leader) {
+#pragma unroll
+          for (int k = decltype(k0)::value; k < decltype(k1)::value; ++k)
+            mma_ts(tO, tP + 8 * k, va + (k * 2048 >> 4), idesc_m128(D, true), j > 0 || k > 0);
+          if (decltype(k1)::value == KT / 16) mma_commit(bar(kBarO + q));
+        }
+      };
+      constexpr std::integral_constant<int, 0> kBegin{};
+      constexpr std::integral_constant<int, KT / 32> kHalf{};
+      constexpr std::integral_constant<int, Geo::kOver ? KT * 3 / 64 : 0> kThird{};
+      constexpr std::integral_constant<int, KT / 16> kEnd{};
+      while (ok) {
+        if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
+        const int n = __shfl_sync(kFull, sh->unit[ru.slot].n, 0);
+        const int i0 = __shfl_sync(kFull, sh->unit[ru.slot].run, 0) * W1 * QT, edge = i0 / KT;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarUEmpty + ru.slot));
+        ru.next(NU);
+        if (n < 0) break;
+        const int mine = key_tiles<KT>(i0, q, W1, n);
+        const int nk = QT == 1 ? mine : max(mine, key_tiles<KT>(i0, 1 - q, W1, n));
+        if (!(ok = warp_wait(bar(kBarQFull), ph_q, stop))) break;
+        ph_q ^= 1u;
+        wait_kv(kv);  // K of tile 0
+        if (mine > 0) score(kv);
+        commit(kBarKVEmpty + kv.slot);
+        if (nk == 1) commit(kBarQEmpty);
+        kv.next(NS);
+        for (int j = 0; j < nk && ok; ++j) {
+          const bool more = j + 1 < nk;
+          const Ring k = kv;  // K of tile j + 1, then V of tile j
+          if (more) kv.next(NS);
+          const Ring v = kv;
+          kv.next(NS);
+          auto next_scores = [&] {
+            if (!more) return;
+            wait_kv(k);
+            if (j + 1 < mine) score(k);
+            commit(kBarKVEmpty + k.slot);
+            if (j + 2 == nk) commit(kBarQEmpty);
+          };
+          if constexpr (!Geo::kOver) next_scores();
+          wait_kv(v);
+          if (!ok) break;
+          if (j >= edge && lane == 0) mbar_arrive(bar(kBarG));  // the guard looks at V while the softmax runs
+          if (j < mine && !(ok = warp_wait(bar((Geo::kOver ? kBarH : kBarP) + q), ph_p, stop))) break;
+          if (j >= edge) {
+            if (!(ok = warp_wait(bar(kBarV), ph_v, stop))) break;
+            ph_v ^= 1u;
           }
+          if (j < mine) {
+            if constexpr (Geo::kOver) {
+              value(v, j, kBegin, kHalf);
+              if (!(ok = warp_wait(bar(kBarI + q), ph_p, stop))) break;
+              value(v, j, kHalf, kThird);
+              if (!(ok = warp_wait(bar(kBarP + q), ph_p, stop))) break;
+            }
+            value(v, j, kThird, kEnd);
+            ph_p ^= 1u;
+          }
+          commit(kBarKVEmpty + v.slot);
+          if constexpr (Geo::kOver) next_scores();
         }
-        if (!warp_wait(bar(kBarUEmpty + r.slot), r.phase ^ 1u, stop)) break;
-        if (lane == 0) {
-          sh->unit[r.slot] = u;
-          sh->odd_v[r.slot] = 0;
-          mbar_arrive(bar(kBarUFull + r.slot));
-        }
-        r.next(2);
-        if (u.n < 0) break;
       }
-    } else if (role == 1) {
+      if (*stop && leader) {  // matrix instructions in flight end before TMEM is freed
+        mma_commit(bar(kBarDrain + q));
+        const long long t0 = global_ns();
+        while (!mbar_try(bar(kBarDrain + q), 0) && global_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    } else if (role == 2) {
       // ------------------------------------------------------------ loads
       if (lane == 0) {
         Ring ru, kv;
@@ -327,7 +424,7 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
           if (!mbar_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
           const Unit u = sh->unit[ru.slot];
           mbar_arrive(bar(kBarUEmpty + ru.slot));
-          ru.next(2);
+          ru.next(NU);
           if (u.n < 0) break;
           const int i0 = u.run * W1 * QT;
           int nk = 0;
@@ -339,9 +436,9 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             for (int c = 0; c < D / 64; ++c)
               tma_load(s0 + Geo::kQ + q * Geo::kQTile + c * kRows * 128, &mq, 64 * c, u.head * G,
                        u.first + i0 + q * W1, bar(kBarQFull));
-          // in the order the MMA warp takes them: K0 .. K(NB-1) V0 K(NB) V1 ...
+          // in the order the MMA warps take them: K0 K1 V0 K2 V1 ...
           auto load = [&](const CUtensorMap* map, int j) {
-            if (!ok || j >= nk || !(ok = mbar_wait(bar(kBarKVFull + NS + kv.slot), kv.phase ^ 1u, stop))) return;
+            if (!ok || j >= nk || !(ok = mbar_wait(bar(kBarKVEmpty + kv.slot), kv.phase ^ 1u, stop))) return;
             mbar_expect_tx(bar(kBarKVFull + kv.slot), Geo::kSlot);
             for (int c = 0; c < D / 64; ++c)
               tma_load(s0 + Geo::kKV + kv.slot * Geo::kSlot + c * KT * 128, map, 64 * c, u.head, u.first + j * KT,
@@ -349,174 +446,102 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             kv.next(NS);
             issued = min(issued + 1, NS);
           };
-          for (int j = 0; j < NB; ++j) load(&mk, j);
+          load(&mk, 0);
           for (int j = 0; j < nk && ok; ++j) {
+            load(&mk, j + 1);
             load(&mv, j);
-            load(&mk, j + NB);
           }
         }
         if (*stop) {  // copies in flight land before the shared memory is given back
           const long long t0 = global_ns();
+          while (issued > 0 && !mbar_try(bar(kBarQFull), ph_q ^ 1u) && global_ns() - t0 < kWaitLimitNs) {
+          }
           for (int i = 0; i < issued; ++i) {
             kv.slot = kv.slot == 0 ? NS - 1 : kv.slot - 1;
             if (kv.slot == NS - 1) kv.phase ^= 1u;
             while (!mbar_try(bar(kBarKVFull + kv.slot), kv.phase) && global_ns() - t0 < kWaitLimitNs) {
             }
           }
-          while (issued > 0 && !mbar_try(bar(kBarQFull), ph_q ^ 1u) && global_ns() - t0 < kWaitLimitNs) {
-          }
         }
       }
-    } else if (role == 0) {
-      // ------------------------------------------------------------ matrix instructions
-      // The whole warp runs this, on values it knows to be uniform, and one
-      // elected lane issues: descriptors then stay in uniform registers (from
-      // a single-lane branch each instruction took about 70 cycles to issue).
-      Ring ru, kv;
-      uint32_t ph_q = 0, ph_p = 0, ph_v = 0;  // ph_p: a bit per P buffer
-      bool ok = true;
-      const bool leader = elect_one();
-      const uint64_t dq = sw128_desc(s0 + Geo::kQ, 0), dk = sw128_desc(s0 + Geo::kKV, 0);
-      const uint64_t dv = sw128_desc(s0 + Geo::kKV, KT * 128);
-      auto commit = [&](int b) {
-        if (leader) mma_commit(bar(b));
-      };
-      // score tile j of query tile q: S = Q_q K^T with K in slot `slot`
-      auto score = [&](int q, int j, int slot) {
-        const int b = 2 * q + j % NB;
-        const uint64_t qa = dq + (q * Geo::kQTile >> 4), ka = dk + (slot * Geo::kSlot >> 4);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tm + Geo::kS + (NB * q + j % NB) * KT, qa + (((k >> 2) * kRows * 128 + (k & 3) * 32) >> 4),
-                   ka + (((k >> 2) * KT * 128 + (k & 3) * 32) >> 4), idesc_m128(KT, false), k != 0);
-          mma_commit(bar(kBarS + b));
-        }
-      };
-      // O_q (+)= P V with V in slot `slot`, half h of the keys
-      auto value = [&](int q, int j, int slot, int h) {
-        const uint64_t va = dv + (slot * Geo::kSlot >> 4);
-        if (leader) {
-#pragma unroll
-          for (int k = h * KT / 32; k < (h + 1) * KT / 32; ++k)
-            mma_ts(tm + Geo::kO + q * D, tm + Geo::kS + (NB * q + j % NB) * KT + 8 * k, va + (k * 2048 >> 4), idesc_m128(D, true),
-                   j > 0 || k > 0);
-          if (h == 1) mma_commit(bar(kBarO + q + j % NB));
-        }
-      };
-      auto wait_kv = [&] {
-        const bool r = warp_wait(bar(kBarKVFull + kv.slot), kv.phase, stop);
-        fence_after();
-        return r;
-      };
-      while (ok) {
-        if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
-        const int n = __shfl_sync(kFull, sh->unit[ru.slot].n, 0);
-        const int i0 = __shfl_sync(kFull, sh->unit[ru.slot].run, 0) * W1 * QT, edge = i0 / KT;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarUEmpty + ru.slot));
-        ru.next(2);
-        if (n < 0) break;
-        const int nkq[2] = {key_tiles<KT>(i0, 0, W1, n), QT == 2 ? key_tiles<KT>(i0, 1, W1, n) : 0};
-        const int nk = max(nkq[0], nkq[1]);
-        if (!(ok = warp_wait(bar(kBarQFull), ph_q, stop))) break;
-        ph_q ^= 1u;
-        // the first NB score tiles; later ones follow the PV that frees their buffer
-        for (int j = 0; j < min(nk, NB); ++j) {
-          if (!(ok = wait_kv())) break;
-#pragma unroll
-          for (int q = 0; q < QT; ++q)
-            if (j < nkq[q]) score(q, j, kv.slot);
-          commit(kBarKVFull + NS + kv.slot);
-          kv.next(NS);
-        }
-        if (!ok) break;
-        if (nk <= NB) commit(kBarQEmpty);
-        for (int j = 0; j < nk; ++j) {
-          const int vslot = kv.slot;
-          if (!(ok = wait_kv())) break;
-          kv.next(NS);
-          bool guarded = j >= edge;  // the guard looks at V while the softmax of the tile runs
-          if (guarded && lane == 0) mbar_arrive(bar(kBarG));
-          bool have_k = false;
-#pragma unroll
-          for (int q = 0; q < QT; ++q) {
-            if (!ok || j >= nkq[q]) continue;
-            const int b = 2 * q + j % NB;
-            ok = warp_wait(bar(kBarH + b), (ph_p >> b) & 1u, stop);
-            if (ok && guarded) {
-              ok = warp_wait(bar(kBarV), ph_v, stop);
-              ph_v ^= 1u;
-              guarded = false;
-            }
-            fence_after();
-            if (!ok) continue;
-            value(q, j, vslot, 0);
-            if (!(ok = warp_wait(bar(kBarP + b), (ph_p >> b) & 1u, stop))) continue;
-            ph_p ^= 1u << b;
-            fence_after();
-            value(q, j, vslot, 1);
-            if (j + NB < nkq[q]) {
-              if (!have_k && !(ok = wait_kv())) continue;
-              have_k = true;
-              score(q, j + NB, kv.slot);
-            }
-          }
-          if (!ok) break;
-          commit(kBarKVFull + NS + vslot);
-          if (j + NB < nk) {
-            commit(kBarKVFull + NS + kv.slot);
-            if (j + NB + 1 == nk) commit(kBarQEmpty);
-            kv.next(NS);
-          }
+    } else if (role == 3) {
+      // ------------------------------------------------------------ units, and the V guard
+      if (blockIdx.x == 0) {
+        for (int s = lane; s < a.num_seqs; s += 32) {
+          const int f = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
+          if (f < 0 || e < f || e > a.total_tokens || e - f > a.max_seq_tokens)
+            report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
         }
       }
-      if (*stop && leader) {  // matrix instructions in flight end before TMEM is freed
-        mma_commit(bar(kBarDrain));
-        const long long t0 = global_ns();
-        while (!mbar_try(bar(kBarDrain), 0) && global_ns() - t0 < kWaitLimitNs) {
+      // Units of this CTA: every gridDim.x-th, in alternating direction (with
+      // units longest first the CTAs end up with about the same work).
+      Ring pub, ru, kv;
+      int round = 0;
+      bool more = true;
+      auto publish = [&] {  // the next unit, or n = -1 after the last
+        Unit u{0, 0, 0, 0, 0};
+        while (u.n == 0) {
+          const long long x = static_cast<long long>(round) * gridDim.x +
+                              ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+          ++round;
+          if (x < pd.units) u = locate_unit(pd, static_cast<int>(x), lane);
+          if (x >= pd.units || (u.n == 0 && a.num_seqs <= kSortedSeqs)) u.n = -1;
         }
-      }
-    } else {
-      // ------------------------------------------------------------ V guard
-      // V of the tiles that hold keys some row does not see: rows past the
-      // sequence and values that are not finite become zero
-      Ring ru, kv;
+        more = u.n > 0;
+        if (!warp_wait(bar(kBarUEmpty + pub.slot), pub.phase ^ 1u, stop)) return;
+        if (lane == 0) {
+          sh->unit[pub.slot] = u;
+          sh->odd_v[pub.slot] = 0;
+          mbar_arrive(bar(kBarUFull + pub.slot));
+        }
+        pub.next(NU);
+      };
+      publish();
+      if (more) publish();
       uint32_t ph_g = 0;
       while (warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) {
         const Unit u = sh->unit[ru.slot];
         const int uslot = ru.slot;
-        ru.next(2);
+        ru.next(NU);
         if (u.n < 0) break;
+        // V of the tiles that hold keys some row does not see: rows past the
+        // sequence and values that are not finite become zero
         const int i0 = u.run * W1 * QT, edge = i0 / KT;
         int nk = 0;
         for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles<KT>(i0, q, W1, u.n));
         bool ok = true;
-        for (int j = 0; j < min(nk, NB); ++j) kv.next(NS);  // K
+        kv.next(NS);  // K of tile 0
         for (int j = 0; j < nk; ++j) {
+          if (j + 1 < nk) kv.next(NS);  // K of tile j + 1
           if (j >= edge) {
             if (!(ok = warp_wait(bar(kBarG), ph_g, stop))) break;
             ph_g ^= 1u;
             uint4* p = reinterpret_cast<uint4*>(smem + Geo::kKV + kv.slot * Geo::kSlot);
-            bool odd = false;
-#pragma unroll 4
+            const int held = min(KT, u.n - j * KT);  // rows of the sequence
+            if (held < KT)
+              for (int c = 0; c < D / 64; ++c)  // (64 channels of a row are 8 x 16 bytes)
+                for (int i = held * 8 + lane; i < KT * 8; i += 32) p[c * KT * 8 + i] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+            // x * 0 is NaN just where x is not finite
+            __half2 probe = __float2half2_rn(0.f);
+#pragma unroll 8
             for (int i = lane; i < Geo::kSlot / 16; i += 32) {
-              const int key = j * KT + ((i >> 3) % KT);
-              uint4 x = p[i];
-              if (key >= u.n) {
-                p[i] = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-              bool bad = false;
+              const uint4 x = p[i];
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7C00u) == 0x7C00u) { w[e] &= 0xFFFF0000u; bad = true; }
-                if ((w[e] & 0x7C000000u) == 0x7C000000u) { w[e] &= 0x0000FFFFu; bad = true; }
-              }
-              if (bad) {
+              for (int e = 0; e < 4; ++e) probe = __hfma2(u32_as_h2(w[e]), __float2half2_rn(0.f), probe);
+            }
+            const bool odd = __any_sync(kFull, __hisnan(__low2half(probe)) || __hisnan(__high2half(probe)));
+            if (odd) {
+              for (int i = lane; i < Geo::kSlot / 16; i += 32) {
+                uint4 x = p[i];
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[e] & 0x7C00u) == 0x7C00u) w[e] &= 0xFFFF0000u;
+                  if ((w[e] & 0x7C000000u) == 0x7C000000u) w[e] &= 0x0000FFFFu;
+                }
                 p[i] = x;
-                odd = true;
               }
             }
             if (odd) sh->odd_v[uslot] = 1;
@@ -524,31 +549,34 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kBarV));
           }
-          kv.next(NS);                   // V
-          if (j + NB < nk) kv.next(NS);  // K
+          kv.next(NS);  // V of tile j
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
+        if (more) publish();
       }
     }
   } else {
     // -------------------------------------------------------------- softmax
-    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(KVQ_RI));
+    if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int q = warp >> 2, row = tid & 127;
     const uint32_t tlane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tO = tm + Geo::kO + q * D + tlane;
+    const uint32_t tS = tm + q * Geo::kTile + tlane, tP = tS + Geo::kP, tO = tm + Geo::kO + q * D + tlane;
     const int T = a.cfg.tile_tokens, wid = min(T, KT), ent = KT / wid;  // keys per mass entry, entries per tile
     float* s_m = reinterpret_cast<float*>(smem + Geo::kStat) + q * 2 * kRows;
     float* s_w = s_m + kRows;
     Ring ru;
-    uint32_t ph_s[2] = {0u, 0u}, ph_o[2] = {0u, 0u};
+    uint32_t ph_s = 0, ph_o = 0, ph_t = q == 0 ? 1u : 0u;  // (query tile 0 has the first turn)
     const bool leader = elect_one();
-    constexpr int HK = KT / 2;  // keys of half a tile
-    while (true) {
-      if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
+    auto publish = [&](int b) {  // this warp's TMEM accesses so far
+      fence_before();
+      __syncwarp();
+      mbar_arrive_if(leader, bar(b + q));
+    };
+    while (warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) {
       const Unit u = sh->unit[ru.slot];
       const int uslot = ru.slot;
-      ru.next(2);
+      ru.next(NU);
       if (u.n < 0) break;
       const int first = u.run * W1 * QT + q * W1;        // the tile's first token
       const int nk = key_tiles<KT>(first, 0, W1, u.n);
@@ -558,41 +586,30 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
       const int masked = first / KT;                     // tiles from here on need the mask
       const long long slot = MASS && nk > 0 ? mass_slot(pd, u, u.run * QT + q) : -1;
       float* scr = pd.scratch + (static_cast<size_t>(blockIdx.x) * QT + q) * pd.max_tiles_k * (ent + 1) * kRows + row;
+      // tiles that both query tiles have: they take turns
+      const int turns = !Geo::kTurns ? 0 : min(nk, key_tiles<KT>(first, q == 0 ? 1 : -1, W1, u.n));
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < nk; ++j) {
-        const int buf = j % NB;
-        const uint32_t tS = tm + Geo::kS + (NB * q + buf) * KT + tlane;
-        if (!(ok = warp_wait(bar(kBarS + 2 * q + buf), ph_s[buf], stop))) break;
-        ph_s[buf] ^= 1u;
+        if (!(ok = warp_wait(bar(kBarS + q), ph_s, stop))) break;
+        ph_s ^= 1u;
         fence_after();
-        // The tile goes in two halves.  The first half's weights are taken
-        // relative to the maximum up to it while the second half's scores are
-        // still on their way and being compared; P V starts on them while the
-        // second half's weights are computed.
         float s[KT];
-        const int lim = vis - j * KT;  // last key of the tile that the row sees
-        // loads of half h, its mask and maximum (times the scale)
-        auto load = [&](auto at) {
-          constexpr int o = decltype(at)::value;
-          tmem_ld32<o>(tS + o, s);
-          if constexpr (HK == 64) tmem_ld32<o + HK - 32>(tS + o + 32, s);
-        };
-        auto top_of = [&](auto at) {
-          constexpr int o = decltype(at)::value;
-          tmem_wait32<o>(s);
-          if constexpr (HK == 64) tmem_wait32<o + HK - 32>(s);
+        // mask of the keys [o, e) and their maximum (times the scale)
+        auto top_of = [&](auto from, auto to) {
+          constexpr int o = decltype(from)::value, e = decltype(to)::value;
           if (j >= masked) {
+            const int lim = vis - j * KT;  // last key of the tile that the row sees
 #pragma unroll
-            for (int c = o; c < o + HK; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
+            for (int c = o; c < e; ++c) s[c] = c <= lim ? s[c] : -INFINITY;
           }
           float mx[4] = {s[o], s[o + 1], s[o + 2], s[o + 3]};
 #pragma unroll
-          for (int c = o + 4; c < o + HK - 4; c += 8)
+          for (int c = o + 4; c < e - 4; c += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3nan(mx[e], s[c + e], s[c + 4 + e]);
+            for (int k = 0; k < 4; ++k) mx[k] = max3nan(mx[k], s[c + k], s[c + 4 + k]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3nan(mx[e], s[o + HK - 4 + e], s[o + HK - 4 + e]);
+          for (int k = 0; k < 4; ++k) mx[k] = max3nan(mx[k], s[e - 4 + k], s[e - 4 + k]);
           const float t = max3nan(mx[0], mx[1], max3nan(mx[2], mx[3], mx[3])) * pd.qscale;
           if (!(t < INFINITY)) l = NAN;  // a NaN or an infinite score: the row is NaN
           return t;
@@ -606,9 +623,9 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             m = top;
             l *= alpha;
           }
-          if (j == 0) return true;
-          // the last PV is done: with one score buffer this tile's score MMA came after it
-          if (NB > 1 && !warp_wait(bar(kBarO + q + (j - 1) % NB), ph_o[(j - 1) % NB] ^ 1u, stop)) return false;
+          if (j == 0) return;
+          // the last P V is done (with P over S this tile's score MMA came after it)
+          if (!Geo::kOver && !(ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop))) return;
           fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) {  // few registers: the scores stay in theirs
@@ -618,72 +635,129 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
             for (int e = 0; e < 8; ++e) o[e] *= alpha;
             tmem_st8(tO + c, o);
           }
-          return true;
         };
         float2 part[KT / 32];  // sums of 32 keys
-        uint32_t p[HK / 2];
-        auto weigh = [&](auto at) {
-          constexpr int o = decltype(at)::value;
+        // weights of the keys [o, e) into p
+        auto weigh = [&](auto from, auto to, auto& p) {
+          constexpr int o = decltype(from)::value, e = decltype(to)::value;
           const float mu = m == -INFINITY ? 0.f : m;  // a row with no finite score so far
           const float2 sc2 = make_float2(pd.qscale, pd.qscale), mu2 = make_float2(-mu, -mu);
 #pragma unroll
-          for (int c = 0; c < HK; c += 2) {
-            const float2 x = __ffma2_rn(make_float2(s[o + c], s[o + c + 1]), sc2, mu2);
-            const float2 e = make_float2(ex2(x.x), ex2(x.y));
-            float2& sum = part[(o + c) / 32];
-            sum = c % 32 == 0 ? e : __fadd2_rn(sum, e);
-            p[c / 2] = h2_as_u32(__float22half2_rn(e));
+          for (int c = o; c < e; c += 2) {
+            const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, mu2);
+            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+            float2& sum = part[c / 32];
+            sum = c % 32 == 0 ? y : __fadd2_rn(sum, y);
+            p[(c - o) / 2] = h2_as_u32(__float22half2_rn(y));
           }
         };
-        // P of 32 keys takes 16 columns of scores already read
-        auto store = [&](int o) {
-          if constexpr (HK == 64) tmem_st32<0>(tS + o / 2, p); else tmem_st16(tS + o / 2, p);
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
+        auto take_turn = [&] {
+          if (Geo::kTurns && j < turns && ok) {
+            ok = warp_wait(bar(kBarT + q), ph_t, stop);
+            ph_t ^= 1u;
+          }
         };
-        constexpr std::integral_constant<int, 0> kFirst{};
-        constexpr std::integral_constant<int, HK> kSecond{};
-        load(kFirst);
-        float top = top_of(kFirst);
-        load(kSecond);
-        if (__any_sync(kFull, top > m + kLazy) && !(ok = grow(top))) break;
-        weigh(kFirst);
-        top = top_of(kSecond);
-        if (__any_sync(kFull, top > m + kLazy)) {  // rare: the first half again
-          if (!(ok = grow(top))) break;
-          weigh(kFirst);
+        auto pass_turn = [&] {
+          if (Geo::kTurns && j < turns) mbar_arrive_if(leader, bar(kBarT + 1 - q));
+        };
+        constexpr std::integral_constant<int, 0> k0{};
+        constexpr std::integral_constant<int, KT / 2> kMid{};
+        constexpr std::integral_constant<int, KT> kEnd{};
+        if constexpr (Geo::kOver) {
+          // The tile goes in two halves.  The first half's weights are taken
+          // relative to the maximum up to it while the second half's scores
+          // are still on their way and being compared; P V starts on them
+          // while the second half's weights are computed.
+          uint32_t pa[KT / 4], pb[KT / 8];
+          constexpr std::integral_constant<int, 32> k32{};
+          constexpr std::integral_constant<int, KT - 32> k96{};
+          constexpr std::integral_constant<int, KT - 16> k112{};
+          tmem_ld32<0>(tS, s);
+          tmem_wait32<0>(s);
+          tmem_ld32<32>(tS + 32, s);
+          tmem_ld32<KT - 64>(tS + KT - 64, s);
+          tmem_ld32<KT - 32>(tS + KT - 32, s);
+          float top = top_of(k0, k32);
+          if (__any_sync(kFull, top > m + kLazy)) grow(top);
+          take_turn();
+          weigh(k0, k32, pa);
+          tmem_wait32<32>(s);
+          tmem_wait32<KT - 64>(s);
+          tmem_wait32<KT - 32>(s);
+          top = top_of(k32, kEnd);
+          if (__any_sync(kFull, top > m + kLazy)) {  // rare: the first run again
+            grow(top);
+            weigh(k0, k32, pa);
+          }
+          if (!ok) break;
+          weigh(k32, kMid, *reinterpret_cast<uint32_t(*)[KT / 8]>(pa + KT / 8));
+          tmem_st32<0>(tP, pa);  // over 32 columns of scores already read
+          weigh(kMid, k96, pb);
+          tmem_wait_st();
+          publish(kBarH);
+          tmem_st16(tP + KT / 4, pb);
+          weigh(k96, k112, pa);
+          pass_turn();
+          tmem_wait_st();
+          publish(kBarI);
+          weigh(k112, kEnd, *reinterpret_cast<uint32_t(*)[KT / 8]>(pa + 8));
+          tmem_st16(tP + KT / 2 - 16, *reinterpret_cast<uint32_t(*)[KT / 8]>(pa));
+        } else {
+          uint32_t p[KT / 2];
+          tmem_ld32<0>(tS, s);
+          tmem_ld32<32>(tS + 32, s);
+          if constexpr (KT == 128) {
+            tmem_ld32<KT - 64>(tS + KT - 64, s);
+            tmem_ld32<KT - 32>(tS + KT - 32, s);
+          }
+          tmem_wait32<0>(s);
+          tmem_wait32<32>(s);
+          if constexpr (KT == 128) {
+            tmem_wait32<KT - 64>(s);
+            tmem_wait32<KT - 32>(s);
+          }
+          publish(kBarF);  // the next scores may come
+          const float top = top_of(k0, kEnd);
+          if (__any_sync(kFull, top > m + kLazy)) grow(top);
+          take_turn();
+          weigh(k0, kEnd, p);
+          pass_turn();
+          // the last P V is done: P may be written
+          if (j > 0 && ok) ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop);
+          if (!ok) break;
+          fence_after();
+          tmem_st32<0>(tP, p);
+          if constexpr (KT == 128) tmem_st32<KT / 2 - 32>(tP + 32, p);
         }
-        store(0);
-        mbar_arrive_if(leader, bar(kBarH + 2 * q + buf));
-        weigh(kSecond);
-        store(HK);
-        mbar_arrive_if(leader, bar(kBarP + 2 * q + buf));
-        ph_o[j % NB] ^= 1u;
+        tmem_wait_st();
+        publish(kBarP);
         const float mu = m == -INFINITY ? 0.f : m;
+        ph_o ^= 1u;
         float ps[KT / 32];
         float all = 0.f;
 #pragma unroll
         for (int k = 0; k < KT / 32; ++k) all += ps[k] = part[k].x + part[k].y;
         l += all;
-        if (MASS && slot >= 0) {
-          float* d = scr + static_cast<size_t>(j) * (ent + 1) * kRows;
-          if (wid == 32) {
+        if constexpr (MASS) {
+          if (slot >= 0) {
+            float* d = scr + static_cast<size_t>(j) * (ent + 1) * kRows;
+            if (wid == 32) {
 #pragma unroll
-            for (int k = 0; k < KT / 32; ++k) d[k * kRows] = ps[k];
-          } else if (wid == 64) {
+              for (int k = 0; k < KT / 32; ++k) d[k * kRows] = ps[k];
+            } else if (wid == 64) {
 #pragma unroll
-            for (int k = 0; k < KT / 64; ++k) d[k * kRows] = ps[2 * k] + ps[2 * k + 1];
-          } else {
-            d[0] = all;
+              for (int k = 0; k < KT / 64; ++k) d[k * kRows] = ps[2 * k] + ps[2 * k + 1];
+            } else {
+              d[0] = all;
+            }
+            d[ent * kRows] = mu;
           }
-          d[ent * kRows] = mu;
         }
       }
       if (!ok) break;
       if (nk > 0) {
         // ---- the tile's rows
-        if (!warp_wait(bar(kBarO + q + (nk - 1) % NB), ph_o[(nk - 1) % NB] ^ 1u, stop)) break;
+        if (!warp_wait(bar(kBarO + q), ph_o ^ 1u, stop)) break;
         fence_after();
         const bool odd = *static_cast<volatile int*>(&sh->odd_v[uslot]) != 0;
         const float inv = 1.f / l;
@@ -726,20 +800,30 @@ __global__ void __launch_bounds__(Geom<D>::kThreads, 1) prompt_kernel(const __gr
           asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
           float* dst = pd.part + static_cast<size_t>(slot) * pd.max_tiles_k * ent;
           const float* base = scr - row;
-          for (int i = row; i < nk * ent; i += kRows) {
-            const float* psum = base + (static_cast<size_t>(i / ent) * (ent + 1) + i % ent) * kRows;
-            const float* pm = base + (static_cast<size_t>(i / ent) * (ent + 1) + ent) * kRows;
+          // four lanes an entry, 32 rows each, then the lanes by butterfly
+          const int rq = (row & 3) * 32;
+          for (int i0 = 0; i0 < nk * ent; i0 += kRows / 4) {
+            const int i = min(i0 + (row >> 2), nk * ent - 1);
+            const float* psum = base + (static_cast<size_t>(i / ent) * (ent + 1) + i % ent) * kRows + rq;
+            const float* pm = base + (static_cast<size_t>(i / ent) * (ent + 1) + ent) * kRows + rq;
+            float4 x[8], y[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x[r] = *reinterpret_cast<const float4*>(psum + 4 * r);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) y[r] = *reinterpret_cast<const float4*>(pm + 4 * r);
             float sum = 0.f;
-#pragma unroll 4
-            for (int r = 0; r < kRows; r += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(psum + r), y = *reinterpret_cast<const float4*>(pm + r);
-              const float4 f = *reinterpret_cast<const float4*>(s_m + r), w = *reinterpret_cast<const float4*>(s_w + r);
-              if (w.x != 0.f) sum += x.x * ex2(y.x - f.x) * w.x;
-              if (w.y != 0.f) sum += x.y * ex2(y.y - f.y) * w.y;
-              if (w.z != 0.f) sum += x.z * ex2(y.z - f.z) * w.z;
-              if (w.w != 0.f) sum += x.w * ex2(y.w - f.w) * w.w;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const float4 f = *reinterpret_cast<const float4*>(s_m + rq + 4 * r);
+              const float4 w = *reinterpret_cast<const float4*>(s_w + rq + 4 * r);
+              if (w.x != 0.f) sum += x[r].x * ex2(y[r].x - f.x) * w.x;
+              if (w.y != 0.f) sum += x[r].y * ex2(y[r].y - f.y) * w.y;
+              if (w.z != 0.f) sum += x[r].z * ex2(y[r].z - f.z) * w.z;
+              if (w.w != 0.f) sum += x[r].w * ex2(y[r].w - f.w) * w.w;
             }
-            dst[i] = sum;
+            sum += __shfl_xor_sync(kFull, sum, 1);
+            sum += __shfl_xor_sync(kFull, sum, 2);
+            if ((row & 3) == 0 && i0 + (row >> 2) < nk * ent) dst[i] = sum;
           }
           asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
         }
@@ -821,9 +905,16 @@ bool make_map(CUtensorMap* m, const void* base, int d, int heads, int tokens, lo
 }
 
 int tile_tokens(const kvq_config& cfg) { return kRows / cfg.group_size; }
-int key_tile(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kKeys : Geom<128>::kKeys; }
-static_assert(Geom<64>::kKeys == Geom<128>::kKeys, "key tiles of d = 64");
-int query_tiles(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256>::kQT : Geom<128>::kQT; }
+int query_tiles(const kvq_config& cfg) { return cfg.head_dim == 256 ? Geom<256, true>::kQT : Geom<128, true>::kQT; }
+// keys per tile of a call with masses
+int mass_keys(const kvq_config& cfg) {
+  switch (cfg.head_dim) {
+    case 64: return Geom<64, true>::kKeys;
+    case 128: return Geom<128, true>::kKeys;
+    default: return Geom<256, true>::kKeys;
+  }
+}
+
 struct PromptSizes {
   long long units;
   int max_tiles_k, window_runs, grid;
@@ -832,7 +923,7 @@ struct PromptSizes {
 PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, int max_seq_tokens, int window,
                          int sms) {
   PromptSizes z;
-  const int W1 = tile_tokens(cfg), keys = key_tile(cfg), ent = keys / std::min(keys, cfg.tile_tokens);
+  const int W1 = tile_tokens(cfg), keys = mass_keys(cfg), ent = keys / std::min(keys, cfg.tile_tokens);
   z.units = prompt_units(cfg, num_seqs, total_tokens);
   z.max_tiles_k = (max_seq_tokens + keys - 1) / keys;
   z.window_runs = window == 0 ? 0 : std::min((window - 1) / W1 + 2, (max_seq_tokens + W1 - 1) / W1);
@@ -846,7 +937,7 @@ PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, 
 
 template <int D, bool MASS>
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
-  using Geo = Geom<D>;
+  using Geo = Geom<D, MASS>;
   static PerDevice known;  // the shared memory is opted in to once per device
   auto kern = prompt_kernel<D, MASS>;
   int sms = 0;
