@@ -57,7 +57,8 @@ constexpr int kSortedSeqs = 1024;
 struct PromptDev {
   PromptArgs a;
   int tile_tokens;     // query tokens per query tile
-  int unit_tokens;     // query tokens per unit (one or two query tiles)
+  int unit_tokens;     // query tokens per unit (one or two query tiles), W
+  uint32_t unit_magic; // floor(2^32 / W) + 1: the high word of x times it is x / W for x < 2^24
   int units;           // host bound on the number of units
   int max_tiles_k;     // key tiles of the longest sequence
   int window_runs;     // query tiles per (sequence, head) that can hold counted queries; 0: all
@@ -66,36 +67,60 @@ struct PromptDev {
   float* part;         // per query tile of the call [max_tiles_k * entries per key tile]
 };
 
+// whether rows [first, end) can be a sequence
+__device__ __forceinline__ bool seq_ok(int first, int end, int total, int longest) {
+  return first >= 0 && end >= first && end <= total && end - first <= longest;
+}
 // Length and first row of sequence s; 0 tokens if the prefix sums are bad.
 __device__ __forceinline__ int seq_len(const PromptArgs& a, int s, int& first) {
   first = a.cu_seqlens[s];
   const int end = a.cu_seqlens[s + 1];
-  const bool ok = first >= 0 && end >= first && end <= a.total_tokens && end - first <= a.max_seq_tokens;
-  return ok ? end - first : 0;
+  return seq_ok(first, end, a.total_tokens, a.max_seq_tokens) ? end - first : 0;
 }
 
 struct Unit {
   int seq, run, head, n, first;  // n = 0: nothing here
 };
 
-// Where unit u sits; the whole warp calls it.  Up to kSortedSeqs sequences:
-// units in descending order of their run index (so of their keys), from a
-// binary search over the levels, count(c) = number of units of run >= c.
+// Finds the units; one warp uses it, all lanes together.
+// Up to kSortedSeqs sequences: units in descending order of their run index
+// (so of their keys), from a binary search over the levels, count(c) = number
+// of runs >= c.  Up to 32 sequences their run counts stay in registers, a lane
+// each (a search took 4000 to 5000 cycles with loads and divisions in it).
 // More: sequence s owns the slots from first_s / W + s on, found by binary
 // search; slots past its units are empty.
-__device__ Unit locate_unit(const PromptDev& pd, int u, int lane) {
-  const PromptArgs& a = pd.a;
-  const int nh = a.cfg.num_kv_heads, W = pd.unit_tokens, B = a.num_seqs;
-  Unit r{0, 0, u % nh, 0, 0};
-  const int x = u / nh;
-  if (B <= kSortedSeqs) {
-    auto count = [&](int c) {
-      int k = 0, f;
-      for (int s = lane; s < B; s += 32) k += max(0, (seq_len(a, s, f) + W - 1) / W - c);
-      return __reduce_add_sync(kFull, k);
-    };
+class UnitFinder {
+ public:
+  // (the numbers are copied: read through a reference to the kernel's
+  // arguments each cost a trip through memory)
+  __device__ UnitFinder(const PromptDev& pd, int lane)
+      : cu_(pd.a.cu_seqlens), seqs_(pd.a.num_seqs), total_(pd.a.total_tokens), longest_(pd.a.max_seq_tokens),
+        heads_(pd.a.cfg.num_kv_heads), W_(pd.unit_tokens), magic_(pd.unit_magic), lane_(lane) {
+    int f;
+    if (lane < seqs_) mine_ = runs(len(lane, f));
+  }
+
+  __device__ Unit find(int u) const {
+    const int x = u / heads_;
+    Unit r{0, 0, u - x * heads_, 0, 0};
+    if (seqs_ > kSortedSeqs) {
+      int lo = 0, hi = seqs_;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (max(cu_[mid], 0) / W_ + mid <= x) lo = mid; else hi = mid;
+      }
+      int f = 0;
+      const int n = len(lo, f);
+      r.run = x - (f / W_ + lo);
+      if (r.run >= 0 && r.run < runs(n)) {
+        r.seq = lo;
+        r.n = n;
+        r.first = f;
+      }
+      return r;
+    }
     if (count(0) <= x) return r;
-    int lo = 0, hi = (a.max_seq_tokens + W - 1) / W, above = 0;
+    int lo = 0, hi = runs(longest_), above = 0;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1, k = count(mid);
       if (k > x) {
@@ -106,38 +131,47 @@ __device__ Unit locate_unit(const PromptDev& pd, int u, int lane) {
       }
     }
     int k = x - above;  // the k-th sequence that has a run `lo`
-    for (int s0 = 0; s0 < B; s0 += 32) {
-      const int s = s0 + lane;
-      int f = 0;
-      const int n = s < B ? seq_len(a, s, f) : 0;
-      const unsigned has = __ballot_sync(kFull, (n + W - 1) / W > lo);
-      if (k < __popc(has)) {
-        const int src = __fns(has, 0, k + 1);
-        r.seq = s0 + src;
+    for (int s0 = 0; s0 < seqs_; s0 += 32) {
+      const bool mine = runs_of(s0 + lane_) > lo;
+      const unsigned has = __ballot_sync(kFull, mine);
+      const unsigned at = __ballot_sync(kFull, mine && __popc(has & ((1u << lane_) - 1u)) == k);
+      if (at != 0) {
+        r.seq = s0 + __ffs(at) - 1;
         r.run = lo;
-        r.n = __shfl_sync(kFull, n, src);
-        r.first = __shfl_sync(kFull, f, src);
+        r.n = len(r.seq, r.first);
         return r;
       }
       k -= __popc(has);
     }
     return r;
   }
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (max(a.cu_seqlens[mid], 0) / W + mid <= x) lo = mid; else hi = mid;
+
+ private:
+  __device__ int len(int s, int& first) const {
+    first = cu_[s];
+    const int end = cu_[s + 1];
+    return seq_ok(first, end, total_, longest_) ? end - first : 0;
   }
-  int f = 0;
-  const int n = seq_len(a, lo, f);
-  r.run = x - (f / W + lo);
-  if (r.run >= 0 && r.run < (n + W - 1) / W) {
-    r.seq = lo;
-    r.n = n;
-    r.first = f;
+  // ceil(n / W), n <= 2^20
+  __device__ int runs(int n) const { return __umulhi(static_cast<uint32_t>(n + W_ - 1), magic_); }
+  __device__ int runs_of(int s) const {
+    int f;
+    if (seqs_ <= 32) return s == lane_ ? mine_ : 0;
+    return s < seqs_ ? runs(len(s, f)) : 0;
   }
-  return r;
-}
+  __device__ int count(int c) const {
+    int k = 0;
+    if (seqs_ <= 32)
+      k = max(0, mine_ - c);
+    else
+      for (int s = lane_; s < seqs_; s += 32) k += max(0, runs_of(s) - c);
+    return __reduce_add_sync(kFull, k);
+  }
+  const int32_t* cu_;
+  int seqs_, total_, longest_, heads_, W_;
+  uint32_t magic_;
+  int lane_, mine_ = 0;
+};
 
 // slot of query tile `run` of u's sequence and head in the partial masses; -1:
 // none of its queries counts
@@ -175,13 +209,14 @@ struct Geom {
   // 608 against 654).
   static constexpr bool kTurns = kOver;
   static constexpr int kSlot = kKeys * D * 2;                                  // one K or V tile
-  static constexpr int kSlots = D == 256 ? 5 : (D == 128 ? 4 : 8);
+  static constexpr int kSlots = D == 64 ? 8 : 4;
   static constexpr int kThreads = kQT * 128 + 128;      // softmax; two MMA warps, loads, V guard and units
   static constexpr int kQTile = kRows * D * 2;
   static constexpr int kQ = 0;
   static constexpr int kKV = kQ + kQT * kQTile;
   static constexpr int kStat = kKV + kSlots * kSlot;    // float m[128], w[128] per query tile (masses)
-  static constexpr int kBar = kStat + kQT * 2 * kRows * 4;
+  static constexpr int kStage = kStat + kQT * 2 * kRows * 4;  // per softmax warp 32 rows x 32 channels fp16
+  static constexpr int kBar = kStage + kQT * 4 * 2048;
   static constexpr int kMisc = kBar + 384;
   static constexpr int kSmem = kMisc + 128 + 1024;      // + alignment slack
   static_assert(kSmem <= 232448, "shared memory per block");
@@ -204,9 +239,7 @@ enum : int {
   kBarP = kBarI + 2,         // [q] all of it is
   kBarO = kBarP + 2,         // [q] its P V is done
   kBarT = kBarO + 2,         // [q] query tile q's turn at the exponentials
-  kBarG = kBarT + 2,         // V of an edge tile has landed: the guard may look at it
-  kBarV,                     // the guard is done with it
-  kBarUFull,                 // [unit slot] a unit is published
+  kBarUFull = kBarT + 2,     // [unit slot] a unit is published
   kBarUEmpty = kBarUFull + kUnitSlots,  // [unit slot] every warp is done with it
   kBarDrain = kBarUEmpty + kUnitSlots,  // [q]
   kBarKVFull = kBarDrain + 2,           // [slot] a K or V tile has landed
@@ -218,6 +251,7 @@ static_assert(kBarCount * 8 <= 384, "barriers fit");
 struct Shared {  // at Geom::kMisc
   uint32_t tmem;
   int stop;
+  int edges, guarded;     // edge tiles, in all, whose V is on its way / that the V guard is done with
   int odd_v[kUnitSlots];  // per unit: V values of an edge tile were left out
   Unit unit[kUnitSlots];
 };
@@ -234,6 +268,28 @@ struct Ring {
     }
   }
 };
+
+// Counters in shared memory, for what may run several steps ahead of its
+// waiter (a barrier's parity would then be ambiguous).  Wait, a whole warp,
+// until the counter has reached `n`; bounded like the barriers' waits.
+__device__ __forceinline__ void set_count(int* counter, int n) {
+  __threadfence_block();
+  *static_cast<volatile int*>(counter) = n;
+}
+__device__ __forceinline__ bool wait_count(const volatile int* counter, int n, volatile int* stop) {
+  if (__all_sync(kFull, *counter >= n)) {
+    __threadfence_block();
+    return true;
+  }
+  const long long t0 = global_ns();
+  bool ok = true;
+  while (ok && *counter < n) {
+    if (global_ns() - t0 > kWaitLimitNs) *stop = 1;
+    ok = !*stop;
+  }
+  __threadfence_block();
+  return __all_sync(kFull, ok);
+}
 
 // The key tiles of a unit's query tile q: tokens [i0 + q W1, ...) of n
 template <int KT>
@@ -279,8 +335,6 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       mbar_init(bar(kBarO + i), 1);
       mbar_init(bar(kBarDrain + i), 1);
     }
-    mbar_init(bar(kBarG), QT);
-    mbar_init(bar(kBarV), 1);
     for (int i = 0; i < NU; ++i) {
       mbar_init(bar(kBarUFull + i), 1);
       mbar_init(bar(kBarUEmpty + i), 4 * QT + QT + 2);
@@ -291,8 +345,21 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
     }
     mbar_init_fence();
     sh->stop = 0;
+    sh->edges = sh->guarded = 0;
   }
   if (warp == 0) tmem_alloc512(smem_u32(&sh->tmem));
+  // the last warp looks up the first unit meanwhile
+  Unit first_unit{0, 0, 0, -1, 0};
+  const UnitFinder finder(pd, lane);
+  if (warp == 4 * QT + 3) {
+    if (lane == 0) {
+      tma_prefetch_map(&mq);
+      tma_prefetch_map(&mk);
+      tma_prefetch_map(&mv);
+    }
+    if (blockIdx.x < pd.units) first_unit = finder.find(blockIdx.x);
+    if (first_unit.n == 0 && a.num_seqs <= kSortedSeqs) first_unit.n = -1;
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -309,7 +376,8 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       // a single-lane branch each instruction took about 70 cycles to issue).
       const int q = role;
       Ring ru, kv;
-      uint32_t ph_q = 0, ph_f = 0, ph_p = 0, ph_v = 0;
+      uint32_t ph_q = 0, ph_f = 0, ph_p = 0;
+      int edges = 0;
       bool ok = true;
       const bool leader = elect_one();
       const uint32_t tS = tm + q * Geo::kTile, tP = tS + Geo::kP, tO = tm + Geo::kO + q * D;
@@ -387,12 +455,8 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           if constexpr (!Geo::kOver) next_scores();
           wait_kv(v);
           if (!ok) break;
-          if (j >= edge && lane == 0) mbar_arrive(bar(kBarG));  // the guard looks at V while the softmax runs
           if (j < mine && !(ok = warp_wait(bar((Geo::kOver ? kBarH : kBarP) + q), ph_p, stop))) break;
-          if (j >= edge) {
-            if (!(ok = warp_wait(bar(kBarV), ph_v, stop))) break;
-            ph_v ^= 1u;
-          }
+          if (j >= edge && !(ok = wait_count(&sh->guarded, ++edges, stop))) break;
           if (j < mine) {
             if constexpr (Geo::kOver) {
               value(v, j, kBegin, kHalf);
@@ -419,14 +483,14 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         Ring ru, kv;
         uint32_t ph_q = 0;
         bool ok = true;
-        int issued = 0;
+        int issued = 0, edges = 0;
         while (ok) {
           if (!mbar_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
           const Unit u = sh->unit[ru.slot];
           mbar_arrive(bar(kBarUEmpty + ru.slot));
           ru.next(NU);
           if (u.n < 0) break;
-          const int i0 = u.run * W1 * QT;
+          const int i0 = u.run * W1 * QT, edge = i0 / KT;
           int nk = 0;
           for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles<KT>(i0, q, W1, u.n));
           if (!(ok = mbar_wait(bar(kBarQEmpty), ph_q ^ 1u, stop))) break;
@@ -443,6 +507,11 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             for (int c = 0; c < D / 64; ++c)
               tma_load(s0 + Geo::kKV + kv.slot * Geo::kSlot + c * KT * 128, map, 64 * c, u.head, u.first + j * KT,
                        bar(kBarKVFull + kv.slot));
+            // the guard may wait for V of an edge tile from now on: the slot's
+            // barrier is in this phase until the MMAs have waited for the guard
+            if (map == &mv && j >= edge) {
+              set_count(&sh->edges, ++edges);
+            }
             kv.next(NS);
             issued = min(issued + 1, NS);
           };
@@ -468,23 +537,21 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       // ------------------------------------------------------------ units, and the V guard
       if (blockIdx.x == 0) {
         for (int s = lane; s < a.num_seqs; s += 32) {
-          const int f = a.cu_seqlens[s], e = a.cu_seqlens[s + 1];
-          if (f < 0 || e < f || e > a.total_tokens || e - f > a.max_seq_tokens)
+          if (!seq_ok(a.cu_seqlens[s], a.cu_seqlens[s + 1], a.total_tokens, a.max_seq_tokens))
             report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
         }
       }
       // Units of this CTA: every gridDim.x-th, in alternating direction (with
       // units longest first the CTAs end up with about the same work).
       Ring pub, ru, kv;
-      int round = 0;
+      int round = 1;
       bool more = true;
-      auto publish = [&] {  // the next unit, or n = -1 after the last
-        Unit u{0, 0, 0, 0, 0};
+      auto publish = [&](Unit u) {  // the next unit from u on, n = -1 after the last
         while (u.n == 0) {
           const long long x = static_cast<long long>(round) * gridDim.x +
                               ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
           ++round;
-          if (x < pd.units) u = locate_unit(pd, static_cast<int>(x), lane);
+          if (x < pd.units) u = finder.find(static_cast<int>(x));
           if (x >= pd.units || (u.n == 0 && a.num_seqs <= kSortedSeqs)) u.n = -1;
         }
         more = u.n > 0;
@@ -496,9 +563,10 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         }
         pub.next(NU);
       };
-      publish();
-      if (more) publish();
-      uint32_t ph_g = 0;
+      const Unit unknown{0, 0, 0, 0, 0};
+      publish(first_unit);
+      if (more) publish(unknown);
+      int edges = 0;
       while (warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) {
         const Unit u = sh->unit[ru.slot];
         const int uslot = ru.slot;
@@ -514,8 +582,9 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         for (int j = 0; j < nk; ++j) {
           if (j + 1 < nk) kv.next(NS);  // K of tile j + 1
           if (j >= edge) {
-            if (!(ok = warp_wait(bar(kBarG), ph_g, stop))) break;
-            ph_g ^= 1u;
+            ++edges;
+            if (!(ok = wait_count(&sh->edges, edges, stop))) break;
+            if (!(ok = warp_wait(bar(kBarKVFull + kv.slot), kv.phase, stop))) break;
             uint4* p = reinterpret_cast<uint4*>(smem + Geo::kKV + kv.slot * Geo::kSlot);
             const int held = min(KT, u.n - j * KT);  // rows of the sequence
             if (held < KT)
@@ -523,15 +592,17 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
                 for (int i = held * 8 + lane; i < KT * 8; i += 32) p[c * KT * 8 + i] = make_uint4(0, 0, 0, 0);
             __syncwarp();
             // x * 0 is NaN just where x is not finite
-            __half2 probe = __float2half2_rn(0.f);
+            const __half2 zero = __float2half2_rn(0.f);
+            __half2 probe[4] = {zero, zero, zero, zero};
 #pragma unroll 8
             for (int i = lane; i < Geo::kSlot / 16; i += 32) {
               const uint4 x = p[i];
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) probe = __hfma2(u32_as_h2(w[e]), __float2half2_rn(0.f), probe);
+              for (int e = 0; e < 4; ++e) probe[e] = __hfma2(u32_as_h2(w[e]), zero, probe[e]);
             }
-            const bool odd = __any_sync(kFull, __hisnan(__low2half(probe)) || __hisnan(__high2half(probe)));
+            const __half2 all = __hadd2(__hadd2(probe[0], probe[1]), __hadd2(probe[2], probe[3]));
+            const bool odd = __any_sync(kFull, __hisnan(__low2half(all)) || __hisnan(__high2half(all)));
             if (odd) {
               for (int i = lane; i < Geo::kSlot / 16; i += 32) {
                 uint4 x = p[i];
@@ -547,13 +618,13 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             if (odd) sh->odd_v[uslot] = 1;
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarV));
+            if (lane == 0) set_count(&sh->guarded, edges);
           }
           kv.next(NS);  // V of tile j
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
-        if (more) publish();
+        if (more) publish(unknown);
       }
     }
   } else {
@@ -565,6 +636,16 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
     const int T = a.cfg.tile_tokens, wid = min(T, KT), ent = KT / wid;  // keys per mass entry, entries per tile
     float* s_m = reinterpret_cast<float*>(smem + Geo::kStat) + q * 2 * kRows;
     float* s_w = s_m + kRows;
+    // token of this row in the query tile, its row in the output from the
+    // tile's first; the same of the piece this lane writes in store k below
+    const int row_token = row / G, own = row_token * nh * G + row % G;
+    int put_token[4], put[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = (warp & 3) * 32 + 8 * k + (lane >> 2);
+      put_token[k] = r < W1 * G ? r / G : 1 << 24;  // (no token)
+      put[k] = ((r / G) * nh * G + r % G) * D + 8 * (lane & 3);
+    }
     Ring ru;
     uint32_t ph_s = 0, ph_o = 0, ph_t = q == 0 ? 1u : 0u;  // (query tile 0 has the first turn)
     const bool leader = elect_one();
@@ -580,7 +661,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       if (u.n < 0) break;
       const int first = u.run * W1 * QT + q * W1;        // the tile's first token
       const int nk = key_tiles<KT>(first, 0, W1, u.n);
-      const int ti = first + row / G;                    // this row's token
+      const int ti = first + row_token;                  // this row's token
       const bool live = row < W1 * G && ti < u.n;
       const int vis = live ? ti : u.n - 1;               // last key this row sees
       const int masked = first / KT;                     // tiles from here on need the mask
@@ -761,38 +842,56 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         fence_after();
         const bool odd = *static_cast<volatile int*>(&sh->odd_v[uslot]) != 0;
         const float inv = 1.f / l;
-        const size_t orow = static_cast<size_t>(u.first + (live ? ti : 0)) * nh * G + u.head * G + row % G;
-        __half* out = static_cast<__half*>(a.out) + orow * D;
+        const size_t base = static_cast<size_t>(u.first + first) * nh * G + u.head * G;  // row 0 of the tile
+        // 32 channels of the warp's 32 rows at a time through shared memory, so
+        // that a store writes 64 bytes of each of eight rows (16 bytes of each
+        // of 32 rows took 2200 to 4300 cycles a tile); 16-byte pieces of a row
+        // are exchanged so that neither side meets bank conflicts
+        unsigned char* stage = smem + Geo::kStage + warp * 2048;
+        __half* out = static_cast<__half*>(a.out) + base * D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32<0>(tO + c, o);
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          float o[64];
+          tmem_ld32<0>(tO + c0, o);
+          tmem_ld32<32>(tO + c0 + 32, o);
           tmem_wait32<0>(o);
-          if (!live) continue;
+          tmem_wait32<32>(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (odd) {  // the values the V guard left out, to the rows that see them
+          for (int e = 0; e < 64; ++e) o[e] *= inv;
+          if (odd && live) {  // the values the V guard left out, to the rows that see them
             for (int key = u.run * W1 * QT / KT * KT; key <= vis; ++key) {
               const __half* vr = static_cast<const __half*>(a.v) + static_cast<size_t>(u.first + key) * a.v_stride +
-                                 u.head * D + c;
+                                 u.head * D + c0;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
+              for (int e = 0; e < 64; ++e) {
                 const float x = __half2float(vr[e]);
                 if (!(fabsf(x) <= 65504.f)) o[e] += x;
               }
             }
           }
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = h2_as_u32(__floats2half2_rn(o[e], o[e + 1]));
-            w.y = h2_as_u32(__floats2half2_rn(o[e + 2], o[e + 3]));
-            w.z = h2_as_u32(__floats2half2_rn(o[e + 4], o[e + 5]));
-            w.w = h2_as_u32(__floats2half2_rn(o[e + 6], o[e + 7]));
-            *reinterpret_cast<uint4*>(out + c + e) = w;
+          for (int c = 0; c < 64; c += 32) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float* x = o + c + 8 * e;
+              uint4 w;
+              w.x = h2_as_u32(__floats2half2_rn(x[0], x[1]));
+              w.y = h2_as_u32(__floats2half2_rn(x[2], x[3]));
+              w.z = h2_as_u32(__floats2half2_rn(x[4], x[5]));
+              w.w = h2_as_u32(__floats2half2_rn(x[6], x[7]));
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ (lane >> 1)) & 3) * 16) = w;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = 8 * k + (lane >> 2);
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + ((lane ^ (r >> 1)) & 3) * 16);
+              if (first + put_token[k] < u.n) *reinterpret_cast<uint4*>(out + put[k] + c0 + c) = w;
+            }
+            __syncwarp();
           }
         }
-        if (live && a.lse != nullptr) a.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+        if (live && a.lse != nullptr) a.lse[base + own] = (m + log2f(l)) * 0.6931471805599453f;
         if (MASS && slot >= 0) {
           const bool counts = live && (a.mass_window == 0 || ti >= u.n - a.mass_window);
           s_m[row] = m == -INFINITY ? 0.f : m;
@@ -956,7 +1055,8 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   PromptDev pd{};
   pd.a = a;
   pd.tile_tokens = tile_tokens(a.cfg);
-  pd.unit_tokens = pd.tile_tokens * Geo::kQT;
+  pd.unit_tokens = pd.tile_tokens * Geo::kQT;  // 16 .. 256
+  pd.unit_magic = static_cast<uint32_t>((1ull << 32) / pd.unit_tokens) + 1;
   pd.units = static_cast<int>(z.units);
   pd.max_tiles_k = z.max_tiles_k;
   pd.window_runs = z.window_runs;
