@@ -21,29 +21,43 @@ struct MassLauncher {
   }
 };
 
-// A warp per tile, lanes over the query heads; the heads of a lane in order,
-// then the lanes by butterfly, so the sum has one fixed order.
+// A warp per kMassTilesPerWarp tiles, lanes over the query heads; the heads of
+// a lane in order, then the lanes by butterfly, so the sum has one fixed order.
+// The tiles' reads are in flight together: the pass is bound by their latency.
 constexpr int kMassTilesPerWarp = 8;
-constexpr int kMassWarps = 8;
+constexpr int kMassWarps = 4;
 __global__ void __launch_bounds__(kMassWarps * 32) decode_mass_kernel(DecodeArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y, T = a.cfg.tile_tokens, hqn = a.cfg.num_kv_heads * a.cfg.group_size;
   const int tiles = (max(a.seq_lens[b], 0) + T - 1) / T;
   const int served = min(tiles, min(a.mass_tiles, a.mass_stat_tiles));
   if (blockIdx.x == 0 && threadIdx.x == 0 && served < tiles) report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
+  const int t0 = (blockIdx.x * kMassWarps + warp) * kMassTilesPerWarp;
+  if (t0 >= served) return;
   const float2* fin = a.mass_final + static_cast<size_t>(b) * hqn;
-  for (int k = 0; k < kMassTilesPerWarp; ++k) {
-    const int t = (blockIdx.x * kMassTilesPerWarp + k) * kMassWarps + warp;
-    if (t >= served) return;
-    const float2* st = a.mass_stats + (static_cast<size_t>(b) * a.mass_stat_tiles + t) * hqn;
-    float sum = 0.f;
-    for (int h = lane; h < hqn; h += 32) {
-      const float2 x = st[h], f = fin[h];
-      if (x.x != 0.f) sum += x.x * exp2f(x.y - f.x) * f.y;  // an empty share has no maximum
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) a.mass[static_cast<size_t>(b) * a.mass_tiles + t] += sum;
+  const float2* st = a.mass_stats + (static_cast<size_t>(b) * a.mass_stat_tiles + t0) * hqn;
+  float* out = a.mass + static_cast<size_t>(b) * a.mass_tiles + t0;
+  const float old = lane < kMassTilesPerWarp && t0 + lane < served ? out[lane] : 0.f;
+  float sum[kMassTilesPerWarp];
+#pragma unroll
+  for (int k = 0; k < kMassTilesPerWarp; ++k) sum[k] = 0.f;
+  for (int h = lane; h < hqn; h += 32) {
+    const float2 f = fin[h];
+    float2 x[kMassTilesPerWarp];
+#pragma unroll
+    for (int k = 0; k < kMassTilesPerWarp; ++k)
+      x[k] = t0 + k < served ? st[static_cast<size_t>(k) * hqn + h] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMassTilesPerWarp; ++k)
+      if (x[k].x != 0.f) sum[k] += x[k].x * exp2f(x[k].y - f.x) * f.y;  // an empty share has no maximum
   }
+  float mine = 0.f;
+#pragma unroll
+  for (int k = 0; k < kMassTilesPerWarp; ++k) {
+    const float s = warp_sum(sum[k]);
+    if (lane == k) mine = s;
+  }
+  if (lane < kMassTilesPerWarp && t0 + lane < served) out[lane] = old + mine;
 }
 
 size_t stats_offset(const kvq_config& cfg, int num_seqs, int num_splits, int sms) {

@@ -940,41 +940,38 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
 }
 
 // mass[s][t] += the partial masses of the query tiles of sequence s that reach
-// tile t.  A CTA per 32 tiles: lanes over the tiles, warps over the (run,
-// head) rows with a fixed stride, then the warps in order.
+// tile t.  A CTA per 32 entries (min(T, KT) keys each): lanes over the
+// entries, warps over the (run, head) rows with a fixed stride, then the warps
+// in order.  The rows of a sequence lie one after another (mass_slot).
 constexpr int kMassWarps = 32;
 __global__ void __launch_bounds__(kMassWarps * 32) prompt_mass_kernel(PromptDev pd, int KT) {
   __shared__ float s_sum[kMassWarps][33];
   const PromptArgs& a = pd.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int s = blockIdx.y, t = blockIdx.x * 32 + lane;
   const int T = a.cfg.tile_tokens, W1 = pd.tile_tokens, nh = a.cfg.num_kv_heads;
-  const int wid = min(T, KT), per = T / wid;  // partial sums per tile of T
-  Unit u{s, 0, 0, 0, 0};
-  u.n = seq_len(a, s, u.first);
-  const int tiles = min((u.n + T - 1) / T, a.max_tiles);
-  if (blockIdx.x * 32 >= tiles) return;
+  const int wid = min(T, KT), per = T / wid;  // keys per entry, entries per tile of T (1 or 2)
+  const int e = blockIdx.x * 32 + lane;
+  Unit u{static_cast<int>(blockIdx.y), 0, 0, 0, 0};
+  u.n = seq_len(a, u.seq, u.first);
+  if (blockIdx.x * 32 * wid >= u.n) return;
   const int w0 = a.mass_window == 0 ? 0 : max(0, u.n - a.mass_window) / W1;
-  const int r0 = max(w0, blockIdx.x * 32 * T / W1), rows = (u.n + W1 - 1) / W1 * nh;
+  const int rows = ((u.n + W1 - 1) / W1 - w0) * nh;  // from query tile w0 on
+  // the first row that sees the entry (rows before it may not have written it)
+  const int from = e * wid < u.n ? max(0, e * wid / W1 - w0) * nh : rows;
   const size_t stride = static_cast<size_t>(pd.max_tiles_k) * (KT / wid);
+  const float* p = pd.part + static_cast<size_t>(mass_slot(pd, u, w0)) * stride + e;
   float sum = 0.f;
-#pragma unroll 4
-  for (int x = r0 * nh + warp; x < rows; x += kMassWarps) {
-    u.head = x % nh;
-    const int run = x / nh;
-    // the key tiles this query tile went over
-    const int held = (min(u.n, (run + 1) * W1) + KT - 1) / KT * (KT / wid);
-    const float* p = pd.part + static_cast<size_t>(mass_slot(pd, u, run)) * stride;
-    for (int k = 0; k < per; ++k)
-      if (t < tiles && t * per + k < held) sum += p[t * per + k];
-  }
+#pragma unroll 8
+  for (int x = warp; x < rows; x += kMassWarps)
+    if (x >= from) sum += p[x * stride];
   s_sum[warp][lane] = sum;
   __syncthreads();
-  if (warp == 0 && t < tiles) {
-    sum = 0.f;
-    for (int w = 0; w < kMassWarps; ++w) sum += s_sum[w][lane];
-    a.mass[static_cast<size_t>(s) * a.max_tiles + t] += sum;
-  }
+  if (warp != 0) return;
+  sum = 0.f;
+  for (int w = 0; w < kMassWarps; ++w) sum += s_sum[w][lane];
+  if (per == 2) sum += __shfl_down_sync(kFull, sum, 1);
+  const int t = e / per;
+  if (e % per == 0 && e * wid < u.n && t < a.max_tiles) a.mass[static_cast<size_t>(u.seq) * a.max_tiles + t] += sum;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1066,8 +1063,8 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   kern<<<z.grid, Geo::kThreads, Geo::kSmem, s>>>(mq, mk, mv, pd);
   e = cudaGetLastError();
   if (e != cudaSuccess || !MASS) return e;
-  const int tiles = std::min(a.max_tiles, (a.max_seq_tokens + a.cfg.tile_tokens - 1) / a.cfg.tile_tokens);
-  prompt_mass_kernel<<<dim3((tiles + 31) / 32, a.num_seqs), kMassWarps * 32, 0, s>>>(pd, Geo::kKeys);
+  const int wid = std::min(a.cfg.tile_tokens, Geo::kKeys);
+  prompt_mass_kernel<<<dim3((a.max_seq_tokens + 32 * wid - 1) / (32 * wid), a.num_seqs), kMassWarps * 32, 0, s>>>(pd, Geo::kKeys);
   return cudaGetLastError();
 }
 

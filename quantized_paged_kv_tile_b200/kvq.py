@@ -177,7 +177,7 @@ def _ptr(t, name, dtype=None, shape=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
@@ -403,11 +403,12 @@ def _rows(t, name, rows, heads, d):
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float16:
         raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if tuple(t.shape) != (rows, heads, d):
+    if t.shape != (rows, heads, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    row, head, element = t.stride()
+    if element != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), heads * d if rows <= 1 else t.stride(0)
+    return t.data_ptr(), heads * d if rows <= 1 else row
 
 
 def prompt_workspace_bytes(cfg: Config, num_seqs: int, total_tokens: int, max_seq_tokens: int,
