@@ -253,5 +253,6 @@ long long generic_prefill_ctas(const kvq_config& cfg, int num_seqs, int max_chun
 cudaError_t launch_selftest_wait_quantize(int32_t* dev_status, cudaStream_t s);
 cudaError_t launch_selftest_wait_decode(int32_t* dev_status, cudaStream_t s);
 cudaError_t launch_selftest_wait_prefill(int32_t* dev_status, cudaStream_t s);
+cudaError_t launch_selftest_wait_prompt(int32_t* dev_status, cudaStream_t s);
 
 }  // namespace kvq

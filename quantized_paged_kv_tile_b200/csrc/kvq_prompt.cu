@@ -8,13 +8,31 @@
 // One pass over the keys with the running maximum m and sum l of the softmax
 // in the log2 domain (c log2 e folded into the exponent's multiply-add).
 //
-// A work unit is (sequence, run of kUnitTokens query tokens, KV head): its
-// 128 rows are tokens x the g query heads of the KV head, token-major, one
-// row per TMEM lane.  Per tile of 128 keys: S = Q K^T (tcgen05, fp32 in
-// TMEM), the softmax of a row in one thread, P as fp16 over S in TMEM, and
-// O += P V with V read as it lies in memory (keys as rows: an MN-major B
-// operand).  P is rounded to fp16 (half a step is 2^-11 of each weight; the
-// sum l takes the unrounded weights), everything else stays in fp32.
+// A query tile is 128 rows, one per TMEM lane: tokens x the g query heads of a
+// KV head, token-major.  A work unit is (sequence, run of one or two query
+// tiles, KV head).  One persistent CTA per SM takes units longest first; its
+// warps pass tiles on through mbarriers:
+//   unit warp      finds the CTA's units and publishes them; as V guard it
+//                  cleans the V tiles that masks reach into
+//   load warp      TMA: the unit's Q tiles, then K and V tiles through a ring
+//   MMA warps      (one per query tile) S = Q K^T and O += P V, tcgen05, fp32
+//                  in TMEM, P as A operand from TMEM, V as it lies in memory
+//                  (keys as rows: an MN-major B operand)
+//   softmax warps  (four per query tile, a row per thread) S from TMEM, running
+//                  maximum and sum in registers, P as fp16 to TMEM, O rescaled
+//                  where the maximum moved far; at the end O / l to memory
+// P is rounded to fp16 (half a step is 2^-11 of each weight; the sum l takes
+// the unrounded weights), everything else stays in fp32.
+//
+// What bounds it: at d = 128 a pair of 128 x 128 tiles needs 2048 cycles of
+// the tensor pipe and 2186 of the exponential unit (measured: 128 exponentials
+// a thread take two warps of a scheduler that long) and takes about 3300, the
+// chain P -> P V -> Q K^T -> S -> maximum -> exponentials of a query tile; long
+// calls run into the power limit first (1567 MHz at 1000 W; a library fp16
+// GEMM of 8192^3 settles at 1287 TFLOP/s there, this kernel at 1050: 16384
+// tokens x 64 heads in 4.18 ms, 1218 TFLOP/s in short runs).  Replacing 1/8 to
+// 3/8 of the exponentials by a polynomial on the FMA pipe gained 1.6% on short
+// runs and lost 4 to 11% on long ones.
 //
 // What a mask hides never reaches a result: masked scores become -inf by
 // selection; V rows past the sequence are zeroed in shared memory; V values
@@ -22,9 +40,11 @@
 // by zero there and added, unweighted, to exactly the rows that see them.
 //
 // Mass (optional): per row and run of T keys the sum of the weights, with the
-// maximum it is relative to, goes to a scratch area of the CTA; once a unit's
-// l and m are final, the rows that count are weighted and summed, and a second
-// kernel adds the units of a sequence to its masses in a fixed order.
+// maximum it is relative to, goes to a scratch area of the CTA; once a query
+// tile's l and m are final, the rows that count are weighted and summed, and a
+// second kernel adds the query tiles of a sequence to its masses in a fixed
+// order.  It costs a fifth of the attention (4096 tokens x 128 heads: 544 us
+// without, 656 with all queries counting).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -350,14 +370,13 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
   if (warp == 0) tmem_alloc512(smem_u32(&sh->tmem));
   // the last warp looks up the first unit meanwhile
   Unit first_unit{0, 0, 0, -1, 0};
-  const UnitFinder finder(pd, lane);
   if (warp == 4 * QT + 3) {
     if (lane == 0) {
       tma_prefetch_map(&mq);
       tma_prefetch_map(&mk);
       tma_prefetch_map(&mv);
     }
-    if (blockIdx.x < pd.units) first_unit = finder.find(blockIdx.x);
+    if (blockIdx.x < pd.units) first_unit = UnitFinder(pd, lane).find(blockIdx.x);
     if (first_unit.n == 0 && a.num_seqs <= kSortedSeqs) first_unit.n = -1;
   }
   fence_before();
@@ -544,6 +563,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       // Units of this CTA: every gridDim.x-th, in alternating direction (with
       // units longest first the CTAs end up with about the same work).
       Ring pub, ru, kv;
+      const UnitFinder finder(pd, lane);
       int round = 1;
       bool more = true;
       auto publish = [&](Unit u) {  // the next unit from u on, n = -1 after the last
@@ -719,7 +739,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         };
         float2 part[KT / 32];  // sums of 32 keys
         // weights of the keys [o, e) into p
-        auto weigh = [&](auto from, auto to, auto& p) {
+        auto weigh = [&](auto from, auto to, uint32_t* p) {
           constexpr int o = decltype(from)::value, e = decltype(to)::value;
           const float mu = m == -INFINITY ? 0.f : m;  // a row with no finite score so far
           const float2 sc2 = make_float2(pd.qscale, pd.qscale), mu2 = make_float2(-mu, -mu);
@@ -742,16 +762,18 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           if (Geo::kTurns && j < turns) mbar_arrive_if(leader, bar(kBarT + 1 - q));
         };
         constexpr std::integral_constant<int, 0> k0{};
-        constexpr std::integral_constant<int, KT / 2> kMid{};
+        constexpr std::integral_constant<int, 32> k32{};
+        constexpr std::integral_constant<int, 64> k64{};
+        constexpr std::integral_constant<int, KT - 32> k96{};
         constexpr std::integral_constant<int, KT> kEnd{};
         if constexpr (Geo::kOver) {
-          // The tile goes in two halves.  The first half's weights are taken
-          // relative to the maximum up to it while the second half's scores
-          // are still on their way and being compared; P V starts on them
-          // while the second half's weights are computed.
+          // The tile goes in runs of keys.  The first 32 keys' weights are
+          // taken relative to the maximum up to them while the other scores
+          // are still on their way and being compared; P V starts on 64 and
+          // then 96 keys while the weights of the rest are computed, and the
+          // other query tile takes its turn before the last 16.  Each part of
+          // P is waited for and published a run later than it is stored.
           uint32_t pa[KT / 4], pb[KT / 8];
-          constexpr std::integral_constant<int, 32> k32{};
-          constexpr std::integral_constant<int, KT - 32> k96{};
           constexpr std::integral_constant<int, KT - 16> k112{};
           tmem_ld32<0>(tS, s);
           tmem_wait32<0>(s);
@@ -771,9 +793,9 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             weigh(k0, k32, pa);
           }
           if (!ok) break;
-          weigh(k32, kMid, *reinterpret_cast<uint32_t(*)[KT / 8]>(pa + KT / 8));
+          weigh(k32, k64, pa + 16);
           tmem_st32<0>(tP, pa);  // over 32 columns of scores already read
-          weigh(kMid, k96, pb);
+          weigh(k64, k96, pb);
           tmem_wait_st();
           publish(kBarH);
           tmem_st16(tP + KT / 4, pb);
@@ -781,7 +803,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           pass_turn();
           tmem_wait_st();
           publish(kBarI);
-          weigh(k112, kEnd, *reinterpret_cast<uint32_t(*)[KT / 8]>(pa + 8));
+          weigh(k112, kEnd, pa + 8);
           tmem_st16(tP + KT / 2 - 16, *reinterpret_cast<uint32_t(*)[KT / 8]>(pa));
         } else {
           uint32_t p[KT / 2];
@@ -1059,7 +1081,23 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------ self-test
+// This file's bounded wait on a barrier that nothing arrives at.
+__global__ void selftest_wait_prompt_kernel(int32_t* dev_status) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int stop;
+  stop = 0;
+  mbar_init(smem_u32(&bar), 1);
+  mbar_init_fence();
+  if (!mbar_wait(smem_u32(&bar), 0, &stop)) report_error(dev_status, KVQ_ERR_DEVICE_TIMEOUT);
+}
+
 }  // namespace
+
+cudaError_t launch_selftest_wait_prompt(int32_t* dev_status, cudaStream_t s) {
+  selftest_wait_prompt_kernel<<<1, 1, 0, s>>>(dev_status);
+  return cudaGetLastError();
+}
 
 long long prompt_units(const kvq_config& cfg, int num_seqs, int total_tokens) {
   return (static_cast<long long>(total_tokens) / (tile_tokens(cfg) * query_tiles(cfg)) + num_seqs) * cfg.num_kv_heads;

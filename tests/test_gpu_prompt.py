@@ -293,3 +293,72 @@ def test_other_stream_and_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(lse, want_lse) and torch.equal(mass, want_mass)
+
+
+def test_offsets_past_32_bits():
+    # 2^31 output elements are passed: the last sequences lie behind them
+    cfg = config(8, 8)
+    n = 262144 + 600
+    lens = [128] * 2048 + [7, 593]
+    q = torch.zeros((n, 64, 128), dtype=torch.float16, device="cuda")
+    k = torch.zeros((n, 8, 128), dtype=torch.float16, device="cuda")
+    v = torch.zeros((n, 8, 128), dtype=torch.float16, device="cuda")
+    tq, tk, tv = rows(cfg, 600, 17)
+    q[-600:], k[-600:], v[-600:] = tq, tk, tv
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((n, 64), 7.0, dtype=torch.float32, device="cuda")
+    kvq.prompt_attention(cfg, q, k, v, out, cu, 593, lse=lse)
+    ref, ref_lse, _, e_out, e_lse, _ = definition(cfg, tq, tk, tv, [7, 593])
+    assert bool(((out[-600:].double() - ref).abs() <= e_out).all())
+    assert bool(((lse[-600:].double() - ref_lse).abs() <= e_lse).all())
+    assert bool((out[:-600] == 0).all())  # values of zero
+    uniform = torch.log(torch.arange(1, 129, device="cuda", dtype=torch.float32))  # scores of zero: ln of the keys seen
+    assert bool(((lse[262016:262144] - uniform[:, None]).abs() < 1e-5).all())
+
+
+def test_calls_at_once_on_two_streams():
+    cfg = config(2, 4)
+    lens = [900, 40, 333]
+    n = sum(lens)
+    data = [rows(cfg, n, 18 + i) for i in range(2)]
+    want = [call(cfg, *x, lens, 0) for x in data]
+    cu = torch.tensor([0, 900, 940, 1273], dtype=torch.int32, device="cuda")
+    need = kvq.prompt_workspace_bytes(cfg, 3, n, 900)
+    sets = [dict(out=torch.zeros_like(want[0][0]), lse=torch.zeros_like(want[0][1]),
+                 mass=torch.zeros_like(want[0][2]), ws=torch.empty(need, dtype=torch.uint8, device="cuda"),
+                 stream=torch.cuda.Stream()) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in sets:
+            with torch.cuda.stream(s["stream"]):
+                s["mass"].zero_()
+        for x, s in zip(data, sets):
+            kvq.prompt_attention(cfg, *x, s["out"], cu, 900, lse=s["lse"], mass=s["mass"], workspace=s["ws"],
+                                 stream=s["stream"])
+    torch.cuda.synchronize()
+    for w, s in zip(want, sets):
+        assert torch.equal(w[0], s["out"]) and torch.equal(w[1], s["lse"]) and torch.equal(w[2], s["mass"])
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    cfg = config(1, 1)
+    q, k, v = rows(cfg, 4, 20)
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    out = torch.zeros(q.shape, dtype=torch.float16, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        kvq.prompt_attention(cfg, q, k, v, out, cu, 4)
+
+
+def test_no_row_and_no_length():
+    cfg = config(1, 2)
+    q, k, v = rows(cfg, 5, 21)
+    out = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda")
+    for cu, top in (([0, 0, 0], 4), ([0], 4), ([0, 5], 0)):
+        kvq.prompt_attention(cfg, q, k, v, out, torch.tensor(cu, dtype=torch.int32, device="cuda"), top)
+    empty = torch.empty((0, 2, 128), dtype=torch.float16, device="cuda")
+    kv = torch.empty((0, 1, 128), dtype=torch.float16, device="cuda")
+    kvq.prompt_attention(cfg, empty, kv, kv, empty, torch.tensor([0, 0], dtype=torch.int32, device="cuda"), 0)
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())
