@@ -84,7 +84,7 @@ def hbm_peak():
 # sources a kernel's code depends on (a change to any of them voids its ncu traffic figure)
 KERNEL_SOURCES = {
     "quantize_tc_kernel": ("kvq_quantize_tc.cu", "kvq_device.cuh", "kvq_internal.h"),
-    "decode_tiles_kernel": ("kvq_decode.cu", "kvq_device.cuh", "kvq_internal.h"),
+    "decode_tiles_kernel": ("kvq_decode_kernel.cuh", "kvq_decode.cu", "kvq_device.cuh", "kvq_internal.h"),
 }
 
 

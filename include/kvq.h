@@ -457,10 +457,14 @@ KVQ_API kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seq
  *                  each sequence; 0: all.  0 without mass.
  *   workspace    : device, >= kvq_prompt_workspace_bytes(...) bytes, with mass
  *                  only (else NULL); contents on entry are ignored.  Calls that
- *                  overlap in time need one each.
- * A row that sees a NaN, or an infinite score, gives NaN; values that a row
- * does not see (later tokens, other sequences, rows behind the last one) never
- * reach it, whatever they are.  A sequence whose prefix sums are negative,
+ *                  overlap in time need one each.  With mass_window = 0 it
+ *                  grows with total_tokens x max_seq_tokens (1.0 GB for
+ *                  131072 tokens, 8 KV heads, g = 8, T = 64), with a window
+ *                  with max_seq_tokens.
+ * A row that sees a NaN, or an infinite score, gives NaN, one that sees an
+ * infinite value gives infinity or NaN there; values that a row does not see
+ * (later tokens, other sequences, rows behind the last one) never reach it,
+ * whatever they are.  A sequence whose prefix sums are negative,
  * descending, past total_tokens or longer than max_seq_tokens is skipped and
  * reported through dev_status (KVQ_ERR_DEVICE_BOUNDS).  All pointers 16-byte
  * aligned; the call is asynchronous on stream. */

@@ -274,9 +274,10 @@ def paged_decode_attention_mass(cfg: Config, q, out, mass, seq_lens, block_table
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
     _on_current_device(q, out, mass, seq_lens, block_tables, k_pool, v_pool, k_tail, v_tail, workspace, dev_status)
     st = load_library().kvq_paged_decode_attention_mass(
-        ctypes.byref(cfg.c()), _ptr(q, "q", torch.float16), _ptr(out, "out", torch.float16),
+        ctypes.byref(cfg.c()), _ptr(q, "q", torch.float16, (b, cfg.num_q_heads, cfg.head_dim)),
+        _ptr(out, "out", torch.float16, (b, cfg.num_q_heads, cfg.head_dim)),
         _ptr(mass, "mass", torch.float32), mass.shape[1], _ptr(seq_lens, "seq_lens", torch.int32), b,
-        _ptr(block_tables, "block_tables", torch.int32), block_tables.shape[1], nb,
+        _ptr(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1])), block_tables.shape[1], nb,
         _ptr(k_pool, "k_pool", torch.uint8), _ptr(v_pool, "v_pool", torch.uint8),
         _ptr(k_tail, "k_tail", torch.float16), _ptr(v_tail, "v_tail", torch.float16), float(softmax_scale),
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), num_splits,

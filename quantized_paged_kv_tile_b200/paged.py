@@ -199,7 +199,8 @@ class PagedKVCache:
                 _in_use(self.mass)
             kvq.prompt_attention(self.cfg, q, k, v, out, cu, longest, lse=lse, mass=self.mass,
                                  mass_window=mass_window, workspace=ws, dev_status=self.dev_status)
-            self.prefill(k.contiguous(), v.contiguous(), lens)
+            if longest > 0:
+                self.prefill(k.contiguous(), v.contiguous(), lens)
         return out
 
     # --------------------------------------------------------------- eviction

@@ -335,3 +335,89 @@ def test_evict_and_decode_captured_on_another_stream():
     got2 = cache.decode(q, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(got2, want2) and torch.equal(cache.mass, ref.mass)
+
+
+@pytest.mark.parametrize("lens", [[0, 0], [5, 0], [0, 64]], ids=str)
+def test_prompts_without_tokens_or_tiles(lens):
+    cfg = config()
+    cache = PagedKVCache(cfg, 2, 256, track_mass=True)
+    q, k, v = rows(cfg, sum(lens), 51)
+    out = cache.prompt(q, k, v, lens)
+    torch.cuda.synchronize()
+    assert cache.status() == 0 and cache.seq_lens.tolist() == lens and out.shape == q.shape
+    for b, n in enumerate(lens):
+        assert abs(float(cache.mass[b].sum()) - n * cfg.num_q_heads) < 1e-3
+    qs, ks, vs = rows(cfg, 2, 52)
+    cache.append(ks, vs)
+    cache.decode(qs)
+    cache.evict(2, 0, 0)
+    assert cache.status() == 0 and cache.seq_lens.tolist() == [n + 1 for n in lens]
+
+
+def test_calls_of_another_shape_or_device_are_refused(monkeypatch):
+    cfg = config()
+    cache = filled(cfg, [100, 100], 53)
+    q = rows(cfg, 2, 54)[0]
+    with pytest.raises(ValueError, match="shape"):
+        cache.decode(q[:1].contiguous())
+    with pytest.raises(kvq.KvqError):
+        cache.evict(1, 1, 1)  # keeps fewer than it protects
+    assert list(cache.host_lens) == [100, 100]
+    with pytest.raises(RuntimeError, match="empty"):
+        cache.prompt(q, q, q, [1, 1])
+    with pytest.raises(ValueError):
+        filled(cfg, [100], track=False).evict(1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        cache.evict(5)
+
+
+FIRST_CALL_IN_A_CAPTURE = """
+import torch
+from quantized_paged_kv_tile_b200 import kvq
+from quantized_paged_kv_tile_b200.paged import PagedKVCache
+cfg = kvq.Config(num_kv_heads=2, group_size=4, tile_tokens=64, bits_k=4, bits_v=4, iters=2)
+cache = PagedKVCache(cfg, 2, 1024, track_mass=True)
+gen = torch.Generator(device="cuda").manual_seed(1)
+q, k, v = (torch.randn((1400, h, 128), generator=gen, device="cuda").half() for h in (8, 2, 2))
+cache.prefill(k, v, [700, 700])
+cu = torch.tensor([0, 700, 1400], dtype=torch.int32, device="cuda")
+out, step = torch.zeros_like(q), torch.zeros_like(q[:2])
+ws = torch.empty(kvq.prompt_workspace_bytes(cfg, 2, 1400, 700), dtype=torch.uint8, device="cuda")
+ews = torch.empty(kvq.evict_workspace_bytes(cfg, 2, 64), dtype=torch.uint8, device="cuda")
+mass = torch.zeros((2, 11), device="cuda")
+args = (cache.block_tables, cache.k_pool, cache.v_pool, cache.k_tail, cache.v_tail, cache.workspace)
+
+def run():
+    kvq.prompt_attention(cfg, q, k, v, out, cu, 700, mass=mass, workspace=ws)
+    kvq.paged_decode_attention_mass(cfg, q[:2], step, cache.mass, cache.seq_lens, *args)
+    kvq.evict_tiles(cfg, cache.mass, cache.seq_lens, cache.block_tables, 4, workspace=ews)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in (out, step, mass, cache.seq_lens, cache.block_tables)]
+again = PagedKVCache(cfg, 2, 1024, track_mass=True)
+again.prefill(k, v, [700, 700])
+cache = again
+args = (cache.block_tables, cache.k_pool, cache.v_pool, cache.k_tail, cache.v_tail, cache.workspace)
+mass.zero_()
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, (out, step, mass, cache.seq_lens, cache.block_tables)))
+assert got[3].tolist() == [4 * 64 + 700 % 64] * 2
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_A_CAPTURE], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert res.returncode == 0 and "same" in res.stdout, res.stdout + res.stderr
