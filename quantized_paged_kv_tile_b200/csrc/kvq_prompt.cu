@@ -10,15 +10,17 @@
 //
 // A query tile is 128 rows, one per TMEM lane: tokens x the g query heads of a
 // KV head, token-major.  A work unit is (sequence, run of one or two query
-// tiles, KV head).  One persistent CTA per SM takes units longest first; its
-// warps pass tiles on through mbarriers:
+// tiles, KV head).  One persistent CTA per SM takes units longest first, in two
+// streams (one at d = 256): a query tile each, or, where there are few units,
+// half of the keys of one query tile each, merged by their log-sum-exp at the
+// end.  Its warps pass tiles on through mbarriers:
 //   unit warp      finds the CTA's units and publishes them; as V guard it
 //                  cleans the V tiles that masks reach into
 //   load warp      TMA: the unit's Q tiles, then K and V tiles through a ring
-//   MMA warps      (one per query tile) S = Q K^T and O += P V, tcgen05, fp32
+//   MMA warps      (one per stream) S = Q K^T and O += P V, tcgen05, fp32
 //                  in TMEM, P as A operand from TMEM, V as it lies in memory
 //                  (keys as rows: an MN-major B operand)
-//   softmax warps  (four per query tile, a row per thread) S from TMEM, running
+//   softmax warps  (four per stream, a row per thread) S from TMEM, running
 //                  maximum and sum in registers, P as fp16 to TMEM, O rescaled
 //                  where the maximum moved far; at the end O / l to memory
 // P is rounded to fp16 (half a step is 2^-11 of each weight; the sum l takes
@@ -259,7 +261,8 @@ enum : int {
   kBarP = kBarI + 2,         // [q] all of it is
   kBarO = kBarP + 2,         // [q] its P V is done
   kBarT = kBarO + 2,         // [q] query tile q's turn at the exponentials
-  kBarUFull = kBarT + 2,     // [unit slot] a unit is published
+  kBarM = kBarT + 2,         // SPLIT: [1] stream 1 is done with a unit, [0] stream 0 has merged it
+  kBarUFull = kBarM + 2,     // [unit slot] a unit is published
   kBarUEmpty = kBarUFull + kUnitSlots,  // [unit slot] every warp is done with it
   kBarDrain = kBarUEmpty + kUnitSlots,  // [q]
   kBarKVFull = kBarDrain + 2,           // [slot] a K or V tile has landed
@@ -281,9 +284,9 @@ static_assert(sizeof(Shared) <= 128, "shared words fit");
 struct Ring {
   int slot = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ void next(int n) {
-    if (++slot == n) {
-      slot = 0;
+  __device__ __forceinline__ void next(int n, int base = 0) {  // n slots from base on
+    if (++slot == base + n) {
+      slot = base;
       phase ^= 1u;
     }
   }
@@ -311,20 +314,36 @@ __device__ __forceinline__ bool wait_count(const volatile int* counter, int n, v
   return __all_sync(kFull, ok);
 }
 
-// The key tiles of a unit's query tile q: tokens [i0 + q W1, ...) of n
-template <int KT>
-__device__ __forceinline__ int key_tiles(int i0, int q, int W1, int n) {
-  const int first = i0 + q * W1;
-  return first < n ? (min(n, first + W1) + KT - 1) / KT : 0;
+// What stream q of a CTA (its MMA warp, its softmax warpgroup, its columns of
+// TMEM) does of a unit that starts at token i0: the key tiles [lo, hi) for the
+// query tile that starts at token `first`.  Usually a stream has a query tile
+// of its own; in SPLIT launches a unit is one query tile and the two streams
+// share out its key tiles, to be merged at the end.
+struct Work {
+  int first, lo, hi;
+  __device__ __forceinline__ int count() const { return hi - lo; }
+};
+template <int KT, bool SPLIT>
+__device__ __forceinline__ Work stream_work(int i0, int q, int W1, int n) {
+  const int first = i0 + (SPLIT ? 0 : q * W1);
+  const int tiles = first < n ? (min(n, first + W1) + KT - 1) / KT : 0;
+  if (!SPLIT) return {first, 0, tiles};
+  const int half = (tiles + 1) / 2;
+  return {first, q == 0 ? 0 : half, q == 0 ? half : tiles};
 }
 
-template <int D, bool MASS>
+template <int D, bool MASS, bool SPLIT>
 __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(const __grid_constant__ CUtensorMap mq,
                                                                             const __grid_constant__ CUtensorMap mk,
                                                                             const __grid_constant__ CUtensorMap mv,
                                                                             const __grid_constant__ PromptDev pd) {
   using Geo = Geom<D, MASS>;
   constexpr int QT = Geo::kQT, NS = Geo::kSlots, KT = Geo::kKeys, NU = kUnitSlots;
+  constexpr int UQ = SPLIT ? 1 : QT;  // query tiles per unit
+  // SPLIT: each stream has half of the K and V slots for its own key tiles, so
+  // that neither waits for tiles the other has still to read
+  constexpr int KS = SPLIT ? NS / 2 : NS;
+  static_assert(!SPLIT || QT == 2, "two streams");
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const PromptArgs& a = pd.a;
@@ -352,6 +371,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       mbar_init(bar(kBarH + i), 4);
       mbar_init(bar(kBarI + i), 4);
       mbar_init(bar(kBarT + i), 4);
+      mbar_init(bar(kBarM + i), 4);
       mbar_init(bar(kBarO + i), 1);
       mbar_init(bar(kBarDrain + i), 1);
     }
@@ -361,7 +381,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
     }
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(kBarKVFull + i), 1);
-      mbar_init(bar(kBarKVEmpty + i), QT);
+      mbar_init(bar(kBarKVEmpty + i), UQ);
     }
     mbar_init_fence();
     sh->stop = 0;
@@ -393,14 +413,14 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       // The whole warp runs this, on values it knows to be uniform, and one
       // elected lane issues: descriptors then stay in uniform registers (from
       // a single-lane branch each instruction took about 70 cycles to issue).
-      const int q = role;
-      Ring ru, kv;
+      const int q = role, base = SPLIT ? q * KS : 0;
+      Ring ru, kv{base};
       uint32_t ph_q = 0, ph_f = 0, ph_p = 0;
       int edges = 0;
       bool ok = true;
       const bool leader = elect_one();
       const uint32_t tS = tm + q * Geo::kTile, tP = tS + Geo::kP, tO = tm + Geo::kO + q * D;
-      const uint64_t dq = sw128_desc(s0 + Geo::kQ + q * Geo::kQTile, 0), dk = sw128_desc(s0 + Geo::kKV, 0);
+      const uint64_t dq = sw128_desc(s0 + Geo::kQ + (SPLIT ? 0 : q) * Geo::kQTile, 0), dk = sw128_desc(s0 + Geo::kKV, 0);
       const uint64_t dv = sw128_desc(s0 + Geo::kKV, KT * 128);
       auto commit = [&](int b) {
         if (leader) mma_commit(bar(b));
@@ -444,38 +464,67 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       while (ok) {
         if (!warp_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
         const int n = __shfl_sync(kFull, sh->unit[ru.slot].n, 0);
-        const int i0 = __shfl_sync(kFull, sh->unit[ru.slot].run, 0) * W1 * QT, edge = i0 / KT;
+        const int i0 = __shfl_sync(kFull, sh->unit[ru.slot].run, 0) * W1 * UQ, edge = i0 / KT;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarUEmpty + ru.slot));
         ru.next(NU);
         if (n < 0) break;
-        const int mine = key_tiles<KT>(i0, q, W1, n);
-        const int nk = QT == 1 ? mine : max(mine, key_tiles<KT>(i0, 1 - q, W1, n));
+        const Work w0 = stream_work<KT, SPLIT>(i0, 0, W1, n), w1 = stream_work<KT, SPLIT>(i0, QT - 1, W1, n);
+        const int mine = q == 0 ? w0.count() : w1.count(), steps = max(w0.count(), w1.count());
         if (!(ok = warp_wait(bar(kBarQFull), ph_q, stop))) break;
         ph_q ^= 1u;
-        wait_kv(kv);  // K of tile 0
-        if (mine > 0) score(kv);
-        commit(kBarKVEmpty + kv.slot);
-        if (nk == 1) commit(kBarQEmpty);
-        kv.next(NS);
-        for (int j = 0; j < nk && ok; ++j) {
-          const bool more = j + 1 < nk;
-          const Ring k = kv;  // K of tile j + 1, then V of tile j
-          if (more) kv.next(NS);
-          const Ring v = kv;
-          kv.next(NS);
+        // The ring holds K of step 0, then K of step j + 1 and V of step j for
+        // j = 0, 1, ...: of the longer stream, or (SPLIT) of this one
+        const int held = SPLIT ? mine : steps;
+        auto place = [&] {
+          const Ring at = kv;
+          kv.next(KS, base);
+          return at;
+        };
+        // the guard's count when V of this stream's step is clean (0: no edge
+        // tile); it takes the edge tiles in the order they are loaded
+        auto guarded = [&](int step) {
+          int until = 0;
+          if constexpr (SPLIT) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const Work& y = x == 0 ? w0 : w1;
+              if (step < y.count() && y.lo + step >= edge) {
+                ++edges;
+                if (x == q) until = edges;
+              }
+            }
+          } else if (step >= edge) {
+            until = ++edges;
+          }
+          return until;
+        };
+        if (held > 0) {
+          const Ring k = place();
+          wait_kv(k);
+          if (mine > 0) score(k);
+          commit(kBarKVEmpty + k.slot);
+        }
+        if (held <= 1) commit(kBarQEmpty);
+        for (int j = 0; j < steps && ok; ++j) {
+          const int until = guarded(j);
+          if (j >= held) continue;
+          const bool more = j + 1 < held;
+          Ring k = kv;
+          if (more) k = place();
+          const Ring v = place();
           auto next_scores = [&] {
             if (!more) return;
             wait_kv(k);
             if (j + 1 < mine) score(k);
             commit(kBarKVEmpty + k.slot);
-            if (j + 2 == nk) commit(kBarQEmpty);
+            if (j + 2 == held) commit(kBarQEmpty);
           };
           if constexpr (!Geo::kOver) next_scores();
           wait_kv(v);
           if (!ok) break;
           if (j < mine && !(ok = warp_wait(bar((Geo::kOver ? kBarH : kBarP) + q), ph_p, stop))) break;
-          if (j >= edge && !(ok = wait_count(&sh->guarded, ++edges, stop))) break;
+          if (until > 0 && !(ok = wait_count(&sh->guarded, until, stop))) break;
           if (j < mine) {
             if constexpr (Geo::kOver) {
               value(v, j, kBegin, kHalf);
@@ -499,55 +548,67 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
     } else if (role == 2) {
       // ------------------------------------------------------------ loads
       if (lane == 0) {
-        Ring ru, kv;
+        Ring ru, ring[2] = {{0}, {SPLIT ? KS : 0}};  // the K and V slots; SPLIT: of each stream
         uint32_t ph_q = 0;
         bool ok = true;
-        int issued = 0, edges = 0;
+        int issued[2] = {0, 0}, edges = 0;
         while (ok) {
           if (!mbar_wait(bar(kBarUFull + ru.slot), ru.phase, stop)) break;
           const Unit u = sh->unit[ru.slot];
           mbar_arrive(bar(kBarUEmpty + ru.slot));
           ru.next(NU);
           if (u.n < 0) break;
-          const int i0 = u.run * W1 * QT, edge = i0 / KT;
-          int nk = 0;
-          for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles<KT>(i0, q, W1, u.n));
+          const int i0 = u.run * W1 * UQ, edge = i0 / KT;
+          const Work w0 = stream_work<KT, SPLIT>(i0, 0, W1, u.n), w1 = stream_work<KT, SPLIT>(i0, QT - 1, W1, u.n);
+          const int steps = max(w0.count(), w1.count());
           if (!(ok = mbar_wait(bar(kBarQEmpty), ph_q ^ 1u, stop))) break;
           ph_q ^= 1u;
-          mbar_expect_tx(bar(kBarQFull), QT * W1 * G * D * 2);
-          for (int q = 0; q < QT; ++q)
+          mbar_expect_tx(bar(kBarQFull), UQ * W1 * G * D * 2);
+          for (int q = 0; q < UQ; ++q)
             for (int c = 0; c < D / 64; ++c)
               tma_load(s0 + Geo::kQ + q * Geo::kQTile + c * kRows * 128, &mq, 64 * c, u.head * G,
                        u.first + i0 + q * W1, bar(kBarQFull));
-          // in the order the MMA warps take them: K0 K1 V0 K2 V1 ...
-          auto load = [&](const CUtensorMap* map, int j) {
-            if (!ok || j >= nk || !(ok = mbar_wait(bar(kBarKVEmpty + kv.slot), kv.phase ^ 1u, stop))) return;
+          auto load_tile = [&](const CUtensorMap* map, int j, int x) {
+            Ring& kv = ring[x];
+            if (!ok || !(ok = mbar_wait(bar(kBarKVEmpty + kv.slot), kv.phase ^ 1u, stop))) return;
             mbar_expect_tx(bar(kBarKVFull + kv.slot), Geo::kSlot);
             for (int c = 0; c < D / 64; ++c)
               tma_load(s0 + Geo::kKV + kv.slot * Geo::kSlot + c * KT * 128, map, 64 * c, u.head, u.first + j * KT,
                        bar(kBarKVFull + kv.slot));
             // the guard may wait for V of an edge tile from now on: the slot's
             // barrier is in this phase until the MMAs have waited for the guard
-            if (map == &mv && j >= edge) {
-              set_count(&sh->edges, ++edges);
+            if (map == &mv && j >= edge) set_count(&sh->edges, ++edges);
+            kv.next(KS, x * KS);
+            issued[x] = min(issued[x] + 1, KS);
+          };
+          auto load = [&](const CUtensorMap* map, int step) {  // in the order the MMA warps take them
+            if constexpr (SPLIT) {
+              if (step < w0.count()) load_tile(map, w0.lo + step, 0);
+              if (step < w1.count()) load_tile(map, w1.lo + step, 1);
+            } else if (step < steps) {
+              load_tile(map, step, 0);
             }
-            kv.next(NS);
-            issued = min(issued + 1, NS);
           };
           load(&mk, 0);
-          for (int j = 0; j < nk && ok; ++j) {
+          for (int j = 0; j < steps && ok; ++j) {
             load(&mk, j + 1);
             load(&mv, j);
           }
         }
         if (*stop) {  // copies in flight land before the shared memory is given back
           const long long t0 = global_ns();
-          while (issued > 0 && !mbar_try(bar(kBarQFull), ph_q ^ 1u) && global_ns() - t0 < kWaitLimitNs) {
+          while (issued[0] > 0 && !mbar_try(bar(kBarQFull), ph_q ^ 1u) && global_ns() - t0 < kWaitLimitNs) {
           }
-          for (int i = 0; i < issued; ++i) {
-            kv.slot = kv.slot == 0 ? NS - 1 : kv.slot - 1;
-            if (kv.slot == NS - 1) kv.phase ^= 1u;
-            while (!mbar_try(bar(kBarKVFull + kv.slot), kv.phase) && global_ns() - t0 < kWaitLimitNs) {
+#pragma unroll
+          for (int x = 0; x < (SPLIT ? 2 : 1); ++x) {
+            Ring& kv = ring[x];
+            for (int i = 0; i < issued[x]; ++i) {
+              if (kv.slot-- == x * KS) {
+                kv.slot = x * KS + KS - 1;
+                kv.phase ^= 1u;
+              }
+              while (!mbar_try(bar(kBarKVFull + kv.slot), kv.phase) && global_ns() - t0 < kWaitLimitNs) {
+              }
             }
           }
         }
@@ -562,7 +623,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       }
       // Units of this CTA: every gridDim.x-th, in alternating direction (with
       // units longest first the CTAs end up with about the same work).
-      Ring pub, ru, kv;
+      Ring pub, ru, ring[2] = {{0}, {SPLIT ? KS : 0}};
       const UnitFinder finder(pd, lane);
       int round = 1;
       bool more = true;
@@ -594,17 +655,25 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         if (u.n < 0) break;
         // V of the tiles that hold keys some row does not see: rows past the
         // sequence and values that are not finite become zero
-        const int i0 = u.run * W1 * QT, edge = i0 / KT;
-        int nk = 0;
-        for (int q = 0; q < QT; ++q) nk = max(nk, key_tiles<KT>(i0, q, W1, u.n));
+        const int i0 = u.run * W1 * UQ, edge = i0 / KT;
+        const Work w0 = stream_work<KT, SPLIT>(i0, 0, W1, u.n), w1 = stream_work<KT, SPLIT>(i0, QT - 1, W1, u.n);
+        const int steps = max(w0.count(), w1.count());
+        auto holds = [&](int step, int x) { return step < (SPLIT ? (x == 0 ? w0 : w1).count() : steps); };
         bool ok = true;
-        kv.next(NS);  // K of tile 0
-        for (int j = 0; j < nk; ++j) {
-          if (j + 1 < nk) kv.next(NS);  // K of tile j + 1
-          if (j >= edge) {
+        for (int step = -1; step < steps && ok; ++step) {
+#pragma unroll
+          for (int x = 0; x < (SPLIT ? 2 : 1); ++x) {
+            Ring& kv = ring[x];
+            if (holds(step + 1, x)) kv.next(KS, x * KS);  // K of step + 1
+            if (step < 0 || !holds(step, x) || !ok) continue;
+            const int j = (SPLIT && x == 1 ? w1.lo : 0) + step;
+            if (j < edge) {
+              kv.next(KS, x * KS);
+              continue;
+            }
             ++edges;
-            if (!(ok = wait_count(&sh->edges, edges, stop))) break;
-            if (!(ok = warp_wait(bar(kBarKVFull + kv.slot), kv.phase, stop))) break;
+            if (!(ok = wait_count(&sh->edges, edges, stop))) continue;
+            if (!(ok = warp_wait(bar(kBarKVFull + kv.slot), kv.phase, stop))) continue;
             uint4* p = reinterpret_cast<uint4*>(smem + Geo::kKV + kv.slot * Geo::kSlot);
             const int held = min(KT, u.n - j * KT);  // rows of the sequence
             if (held < KT)
@@ -639,8 +708,8 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             fence_async_smem();
             __syncwarp();
             if (lane == 0) set_count(&sh->guarded, edges);
+            kv.next(KS, x * KS);
           }
-          kv.next(NS);  // V of tile j
         }
         if (!ok) break;
         if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
@@ -667,6 +736,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       put[k] = ((r / G) * nh * G + r % G) * D + 8 * (lane & 3);
     }
     Ring ru;
+    uint32_t ph_m = 0;
     uint32_t ph_s = 0, ph_o = 0, ph_t = q == 0 ? 1u : 0u;  // (query tile 0 has the first turn)
     const bool leader = elect_one();
     auto publish = [&](int b) {  // this warp's TMEM accesses so far
@@ -679,19 +749,20 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       const int uslot = ru.slot;
       ru.next(NU);
       if (u.n < 0) break;
-      const int first = u.run * W1 * QT + q * W1;        // the tile's first token
-      const int nk = key_tiles<KT>(first, 0, W1, u.n);
+      const Work w = stream_work<KT, SPLIT>(u.run * W1 * UQ, q, W1, u.n);
+      const int first = w.first, nk = w.count();         // the query tile's first token; this stream's key tiles
       const int ti = first + row_token;                  // this row's token
       const bool live = row < W1 * G && ti < u.n;
       const int vis = live ? ti : u.n - 1;               // last key this row sees
       const int masked = first / KT;                     // tiles from here on need the mask
-      const long long slot = MASS && nk > 0 ? mass_slot(pd, u, u.run * QT + q) : -1;
-      float* scr = pd.scratch + (static_cast<size_t>(blockIdx.x) * QT + q) * pd.max_tiles_k * (ent + 1) * kRows + row;
-      // tiles that both query tiles have: they take turns
-      const int turns = !Geo::kTurns ? 0 : min(nk, key_tiles<KT>(first, q == 0 ? 1 : -1, W1, u.n));
+      const long long slot = MASS && nk > 0 ? mass_slot(pd, u, u.run * UQ + (SPLIT ? 0 : q)) : -1;
+      float* scr = pd.scratch + (static_cast<size_t>(blockIdx.x) * QT + (SPLIT ? 0 : q)) * pd.max_tiles_k * (ent + 1) * kRows + row;
+      // tiles that both streams have: they take turns
+      const int turns = !Geo::kTurns ? 0 : min(nk, stream_work<KT, SPLIT>(u.run * W1 * UQ, 1 - q, W1, u.n).count());
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < nk; ++j) {
+      for (int step = 0; step < nk; ++step) {
+        const int j = w.lo + step;  // key tile
         if (!(ok = warp_wait(bar(kBarS + q), ph_s, stop))) break;
         ph_s ^= 1u;
         fence_after();
@@ -724,7 +795,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             m = top;
             l *= alpha;
           }
-          if (j == 0) return;
+          if (step == 0) return;
           // the last P V is done (with P over S this tile's score MMA came after it)
           if (!Geo::kOver && !(ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop))) return;
           fence_after();
@@ -753,13 +824,13 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           }
         };
         auto take_turn = [&] {
-          if (Geo::kTurns && j < turns && ok) {
+          if (Geo::kTurns && step < turns && ok) {
             ok = warp_wait(bar(kBarT + q), ph_t, stop);
             ph_t ^= 1u;
           }
         };
         auto pass_turn = [&] {
-          if (Geo::kTurns && j < turns) mbar_arrive_if(leader, bar(kBarT + 1 - q));
+          if (Geo::kTurns && step < turns) mbar_arrive_if(leader, bar(kBarT + 1 - q));
         };
         constexpr std::integral_constant<int, 0> k0{};
         constexpr std::integral_constant<int, 32> k32{};
@@ -826,7 +897,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           weigh(k0, kEnd, p);
           pass_turn();
           // the last P V is done: P may be written
-          if (j > 0 && ok) ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop);
+          if (step > 0 && ok) ok = warp_wait(bar(kBarO + q), ph_o ^ 1u, stop);
           if (!ok) break;
           fence_after();
           tmem_st32<0>(tP, p);
@@ -858,7 +929,35 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         }
       }
       if (!ok) break;
-      if (nk > 0) {
+      float part0 = 1.f, part1 = 0.f;  // SPLIT: the streams' shares of the merged row
+      bool other = false;              // stream 1 has some
+      if constexpr (SPLIT) {
+        float* s_m1 = reinterpret_cast<float*>(smem + Geo::kStat) + 2 * kRows;  // stream 1's m and l
+        float* s_l1 = s_m1 + kRows;
+        if (q == 1) {
+          if (nk > 0) {
+            if (!warp_wait(bar(kBarO + 1), ph_o ^ 1u, stop)) break;
+            s_m1[row] = m;
+            s_l1[row] = l;
+          }
+          __threadfence_block();
+          publish(kBarM);
+          if (!warp_wait(bar(kBarM), ph_m, stop)) break;  // merged: O and the scratch are free again
+          ph_m ^= 1u;
+        } else {
+          other = stream_work<KT, SPLIT>(u.run * W1 * UQ, 1, W1, u.n).count() > 0;
+          if (!warp_wait(bar(kBarM + 1), ph_m, stop)) break;
+          ph_m ^= 1u;
+          if (other) {  // the log-sum-exp merge of the two
+            const float m1 = s_m1[row], top = fmaxf(m, m1);
+            part0 = m == -INFINITY ? 0.f : ex2(m - top);
+            part1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+            l = l * part0 + s_l1[row] * part1;
+            m = top;
+          }
+        }
+      }
+      if (nk > 0 && (!SPLIT || q == 0)) {
         // ---- the tile's rows
         if (!warp_wait(bar(kBarO + q), ph_o ^ 1u, stop)) break;
         fence_after();
@@ -878,10 +977,21 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           tmem_ld32<32>(tO + c0 + 32, o);
           tmem_wait32<0>(o);
           tmem_wait32<32>(o);
+          if constexpr (SPLIT) {
+            if (other) {
+#pragma unroll
+              for (int c = 0; c < 64; c += 8) {
+                float x[8];
+                tmem_ld8(tO + D + c0 + c, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[c + e] = o[c + e] * part0 + x[e] * part1;
+              }
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 64; ++e) o[e] *= inv;
           if (odd && live) {  // the values the V guard left out, to the rows that see them
-            for (int key = u.run * W1 * QT / KT * KT; key <= vis; ++key) {
+            for (int key = u.run * W1 * UQ / KT * KT; key <= vis; ++key) {
               const __half* vr = static_cast<const __half*>(a.v) + static_cast<size_t>(u.first + key) * a.v_stride +
                                  u.head * D + c0;
 #pragma unroll
@@ -928,8 +1038,9 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           // a row that does not count has weight 0, and its sums may be anything
           auto term = [](float x, float y, float f, float w) { return w != 0.f ? x * ex2(y - f) * w : 0.f; };
           const int stride = (ent + 1) * kRows, ent_bits = ent == 4 ? 2 : ent - 1;
+          const int entries = (SPLIT ? (min(u.n, first + W1) + KT - 1) / KT : nk) * ent;
 #pragma unroll 4
-          for (int i = warp & 3; i < nk * ent; i += 4) {
+          for (int i = warp & 3; i < entries; i += 4) {
             const float* tile = base + static_cast<size_t>(i >> ent_bits) * stride + 4 * lane;
             const float4 x = *reinterpret_cast<const float4*>(tile + (i & (ent - 1)) * kRows);
             const float4 y = *reinterpret_cast<const float4*>(tile + ent * kRows);
@@ -940,6 +1051,9 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
         }
         fence_before();
+      }
+      if constexpr (SPLIT) {
+        if (q == 0) publish(kBarM);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarUEmpty + uslot));
@@ -1026,6 +1140,7 @@ int mass_keys(const kvq_config& cfg) {
 
 struct PromptSizes {
   long long units;
+  bool split;  // a unit is one query tile, its key tiles shared out over two streams
   int max_tiles_k, window_runs, grid;
   size_t scratch_floats, part_floats;
 };
@@ -1034,6 +1149,17 @@ PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, 
   PromptSizes z;
   const int W1 = tile_tokens(cfg), keys = mass_keys(cfg), ent = keys / std::min(keys, cfg.tile_tokens);
   z.units = prompt_units(cfg, num_seqs, total_tokens);
+  // With no more units than SMs a call takes as long as its longest unit: then
+  // a unit is one query tile and the CTA's two streams take half of its keys
+  // each.  Pairs of query tiles against halves of the keys, us (d, heads,
+  // tokens), up to 148 units of pairs: 128, 2 over 1, 1024: 27 / 21; 3093: 53 /
+  // 38; 128, 8 over 1, 4736 (148 units): 95 / 72; 128, 16 over 2, 2368 (148):
+  // 60 / 50; 64, 4 over 1, 6400: 94 / 57; and beyond, where CTAs take several
+  // units and a pair loads each key tile once for two: 128, 16 over 2, 3000
+  // (188): 72 / 71; 4096 (256): 80 / 95; 8192: 239 / 277; 64, 16 over 2, 4096
+  // (256): 71 / 76.
+  z.split = query_tiles(cfg) == 2 && z.units <= sms;
+  if (z.split) z.units = (static_cast<long long>(total_tokens) / W1 + num_seqs) * cfg.num_kv_heads;
   z.max_tiles_k = (max_seq_tokens + keys - 1) / keys;
   z.window_runs = window == 0 ? 0 : std::min((window - 1) / W1 + 2, (max_seq_tokens + W1 - 1) / W1);
   z.grid = static_cast<int>(std::min<long long>(z.units, sms));
@@ -1044,16 +1170,27 @@ PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, 
   return z;
 }
 
+template <int D, bool MASS, bool SPLIT>
+cudaError_t launch_prompt_kernel(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                 const PromptDev& pd, int grid, cudaStream_t s) {
+  using Geo = Geom<D, MASS>;
+  static PerDevice opted_in;  // to the shared memory, once per device
+  auto kern = prompt_kernel<D, MASS, SPLIT>;
+  int done = 0;
+  const cudaError_t e = opted_in.get(&done, [&](int* v) {
+    *v = 1;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  kern<<<grid, Geo::kThreads, Geo::kSmem, s>>>(mq, mk, mv, pd);
+  return cudaGetLastError();
+}
+
 template <int D, bool MASS>
 cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   using Geo = Geom<D, MASS>;
-  static PerDevice known;  // the shared memory is opted in to once per device
-  auto kern = prompt_kernel<D, MASS>;
   int sms = 0;
-  cudaError_t e = known.get(&sms, [&](int* v) {
-    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);
-    return r != cudaSuccess ? r : device_sm_count(v);
-  });
+  cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   const PromptSizes z = prompt_sizes(a.cfg, a.num_seqs, a.total_tokens, a.max_seq_tokens, a.mass_window, sms);
   const int G = a.cfg.group_size, nh = a.cfg.num_kv_heads;
@@ -1065,7 +1202,7 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   PromptDev pd{};
   pd.a = a;
   pd.tile_tokens = tile_tokens(a.cfg);
-  pd.unit_tokens = pd.tile_tokens * Geo::kQT;  // 16 .. 256
+  pd.unit_tokens = pd.tile_tokens * (z.split ? 1 : Geo::kQT);  // 16 .. 256
   pd.unit_magic = static_cast<uint32_t>((1ull << 32) / pd.unit_tokens) + 1;
   pd.units = static_cast<int>(z.units);
   pd.max_tiles_k = z.max_tiles_k;
@@ -1073,8 +1210,11 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
   pd.qscale = a.softmax_scale * kLog2e;
   pd.scratch = static_cast<float*>(a.workspace);
   pd.part = pd.scratch + z.scratch_floats;
-  kern<<<z.grid, Geo::kThreads, Geo::kSmem, s>>>(mq, mk, mv, pd);
-  e = cudaGetLastError();
+  if constexpr (Geo::kQT == 2)
+    e = z.split ? launch_prompt_kernel<D, MASS, true>(mq, mk, mv, pd, z.grid, s)
+                : launch_prompt_kernel<D, MASS, false>(mq, mk, mv, pd, z.grid, s);
+  else
+    e = launch_prompt_kernel<D, MASS, false>(mq, mk, mv, pd, z.grid, s);
   if (e != cudaSuccess || !MASS) return e;
   const int wid = std::min(a.cfg.tile_tokens, Geo::kKeys);
   prompt_mass_kernel<<<dim3((a.max_seq_tokens + 32 * wid - 1) / (32 * wid), a.num_seqs), kMassWarps * 32, 0, s>>>(pd, Geo::kKeys);

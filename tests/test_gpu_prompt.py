@@ -168,6 +168,28 @@ def test_padded_rows_and_strides():
     check(cfg, *rows(cfg, sum(lens), 7, pad=8), lens, window=0)
 
 
+@pytest.mark.parametrize("g", [1, 3, 4, 8])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_many_sequences(d, g):
+    # enough work for every SM: units of two query tiles
+    cfg = config(2, g, d, t=32)
+    lens = [300, 7, 140, 0, 129, 64, 1] * 16
+    check(cfg, *rows(cfg, sum(lens), 22), lens, window=0)
+    lens = [1100, 700, 1333, 64, 1]
+    cfg = config(2, 8, d)
+    check(cfg, *rows(cfg, sum(lens), 25, std=4.0), lens, window=0)
+    check(cfg, *rows(cfg, sum(lens), 26), lens, window=150)
+
+
+@pytest.mark.parametrize("n", [129, 250, 384, 385, 900, 1500])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_over_many_keys(d, n):
+    # less work than SMs: a query tile's keys go to two streams
+    cfg = config(1, 2, d)
+    check(cfg, *rows(cfg, n, 23, std=4.0), [n], window=0)
+    check(cfg, *rows(cfg, n, 24), [n], window=20)
+
+
 def test_long_and_many():
     cfg = config(1, 8)
     check(cfg, *rows(cfg, 3000, 8), [3000], window=0)
@@ -189,16 +211,24 @@ def test_hidden_values_stay_hidden(d, bad):
     """Later tokens, the next sequence and rows in no sequence hold values that
     would spoil everything they reach: the rows that do not see them keep the
     bits they have without them."""
-    cfg = config(1, 4, d)
-    lens, cu = [150, 70], [3, 153, 223]
-    n = 240  # rows 0..2 and 223..239 are in no sequence
+    hidden_values(config(1, 4, d), bad, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_hidden_values_stay_hidden_among_many(d):
+    hidden_values(config(2, 4, d), math.nan, 100)
+
+
+def hidden_values(cfg, bad, more):
+    lens, cu = [150, 70] + [1] * more, [3, 153] + list(range(223, 224 + more))
+    n = 240 + more  # rows 0..2 and the last 17 are in no sequence
     q, k, v = rows(cfg, n, 11)
     clean_k, clean_v = k.clone(), v.clone()
     want, want_lse, want_mass, status = call(cfg, q, clean_k, clean_v, lens, 0, cu=cu, max_len=150)
     assert status == 0
     for x in (k, v):
         x[:3] = bad
-        x[223:] = bad
+        x[223 + more:] = bad
         x[3 + 100] = bad          # token 100 of the first sequence
         x[153 + 69] = bad         # the last token of the second
     got, got_lse, _, status = call(cfg, q, k, v, lens, 0, cu=cu, max_len=150)
@@ -207,7 +237,7 @@ def test_hidden_values_stay_hidden(d, bad):
     seen[3 + 100:153] = True
     seen[153 + 69] = True
     inside = torch.zeros(n, dtype=torch.bool)
-    inside[3:223] = True
+    inside[3:223 + more] = True
     clean = (inside & ~seen).cuda()
     assert torch.equal(got[clean], want[clean]) and torch.equal(got_lse[clean], want_lse[clean])
     assert bool((got[~inside.cuda()] == 7.0).all()) and bool((got_lse[~inside.cuda()] == 7.0).all())
