@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
+import operator
 import os
 
 import torch
@@ -197,6 +199,20 @@ def _on_current_device(*tensors) -> None:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
+def _int(x, name) -> int:
+    """An integer argument as the library takes it (ctypes would wrap a larger one)."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} {x} does not fit 32 bits")
+    return x
+
+
+@functools.lru_cache(maxsize=64)
+def _page_bytes(cfg: Config) -> tuple[int, int]:
+    lay = get_layout(cfg)
+    return lay["page_bytes_k"], lay["page_bytes_v"]
+
+
 def quantize_tiles(cfg: Config, src_k, src_v, tile_desc, block_tables, k_pool, v_pool,
                    num_blocks: int | None = None, dev_status=None, stream=None) -> None:
     """Write path (prefill): quantize the tiles listed in ``tile_desc``
@@ -272,14 +288,18 @@ def paged_decode_attention_mass(cfg: Config, q, out, mass, seq_lens, block_table
     b = seq_lens.shape[0]
     if mass.dim() != 2 or mass.shape[0] != b:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
+    for pool, size in zip((k_pool, v_pool), _page_bytes(cfg)):
+        if pool.numel() < nb * cfg.num_kv_heads * size:
+            raise ValueError(f"a pool of {pool.numel()} bytes holds no {nb} blocks of {cfg.num_kv_heads} x {size}")
     _on_current_device(q, out, mass, seq_lens, block_tables, k_pool, v_pool, k_tail, v_tail, workspace, dev_status)
+    tail = (b, cfg.num_kv_heads, cfg.tile_tokens, cfg.head_dim)
     st = load_library().kvq_paged_decode_attention_mass(
         ctypes.byref(cfg.c()), _ptr(q, "q", torch.float16, (b, cfg.num_q_heads, cfg.head_dim)),
         _ptr(out, "out", torch.float16, (b, cfg.num_q_heads, cfg.head_dim)),
         _ptr(mass, "mass", torch.float32), mass.shape[1], _ptr(seq_lens, "seq_lens", torch.int32), b,
         _ptr(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1])), block_tables.shape[1], nb,
         _ptr(k_pool, "k_pool", torch.uint8), _ptr(v_pool, "v_pool", torch.uint8),
-        _ptr(k_tail, "k_tail", torch.float16), _ptr(v_tail, "v_tail", torch.float16), float(softmax_scale),
+        _ptr(k_tail, "k_tail", torch.float16, tail), _ptr(v_tail, "v_tail", torch.float16, tail), float(softmax_scale),
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), num_splits,
         _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
     _check(st, "kvq_paged_decode_attention_mass")
@@ -305,8 +325,9 @@ def evict_tiles(cfg: Config, mass, seq_lens, block_tables, keep_tiles: int, sink
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
     _on_current_device(mass, seq_lens, block_tables, kept, workspace, dev_status)
     st = load_library().kvq_evict_tiles(
-        ctypes.byref(cfg.c()), _ptr(mass, "mass", torch.float32), mass.shape[1], int(keep_tiles), int(sink_tiles),
-        int(recent_tiles), _ptr(seq_lens, "seq_lens", torch.int32), b,
+        ctypes.byref(cfg.c()), _ptr(mass, "mass", torch.float32), mass.shape[1],
+        _int(keep_tiles, "keep_tiles"), _int(sink_tiles, "sink_tiles"), _int(recent_tiles, "recent_tiles"),
+        _ptr(seq_lens, "seq_lens", torch.int32), b,
         _ptr(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1])), block_tables.shape[1],
         _ptr(kept, "kept", torch.int32, tuple(mass.shape)), _ptr(workspace, "workspace", torch.uint8),
         0 if workspace is None else workspace.numel(), _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
@@ -409,7 +430,7 @@ def _rows(t, name, rows, heads, d):
     row, head, element = t.stride()
     if element != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), heads * d if rows <= 1 else row
+    return t.data_ptr(), heads * d if rows <= 1 else _int(row, f"{name}'s row stride")
 
 
 def prompt_workspace_bytes(cfg: Config, num_seqs: int, total_tokens: int, max_seq_tokens: int,
@@ -443,9 +464,10 @@ def prompt_attention(cfg: Config, q, k, v, out, cu_seqlens, max_seq_tokens: int,
         ctypes.byref(cfg.c()), qp, qs, kp, ks, vp, vs,
         _ptr(out, "out", torch.float16, (n, cfg.num_q_heads, cfg.head_dim)),
         _ptr(lse, "lse", torch.float32, (n, cfg.num_q_heads)), _ptr(cu_seqlens, "cu_seqlens", torch.int32), b, n,
-        int(max_seq_tokens), float(softmax_scale), _ptr(mass, "mass", torch.float32),
-        0 if mass is None else mass.shape[1], int(mass_window), _ptr(workspace, "workspace", torch.uint8),
-        0 if workspace is None else workspace.numel(), _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
+        _int(max_seq_tokens, "max_seq_tokens"), float(softmax_scale), _ptr(mass, "mass", torch.float32),
+        0 if mass is None else mass.shape[1], _int(mass_window, "mass_window"),
+        _ptr(workspace, "workspace", torch.uint8), 0 if workspace is None else workspace.numel(),
+        _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
     _check(st, "kvq_prompt_attention")
 
 

@@ -67,3 +67,12 @@ def test_decode_mass_arguments_that_need_no_device(lib):
     for bad in ((-1, 8, 1), (1, 0, 1), (1, 8, -1)):
         assert lib.kvq_decode_mass_workspace_bytes(ctypes.byref(c), *bad, ctypes.byref(out)) == kvq.KVQ_ERR_INVALID_ARG
     assert lib.kvq_decode_mass_workspace_bytes(ctypes.byref(c), 1, 8, 1, None) == kvq.KVQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [2 ** 31, 2 ** 32, 2 ** 63 - 1, -2 ** 31 - 1])
+def test_integers_are_not_wrapped(bad):
+    with pytest.raises(ValueError, match="keep_tiles"):
+        kvq._int(bad, "keep_tiles")
+    with pytest.raises(TypeError):
+        kvq._int(1.5, "keep_tiles")
+    assert kvq._int(2 ** 31 - 1, "keep_tiles") == 2 ** 31 - 1

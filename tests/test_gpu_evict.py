@@ -337,6 +337,25 @@ def test_evict_and_decode_captured_on_another_stream():
     assert torch.equal(got, want) and torch.equal(got2, want2) and torch.equal(cache.mass, ref.mass)
 
 
+def test_counts_past_32_bits_and_small_buffers_are_refused():
+    cfg = config()
+    cache = filled(cfg, [300, 100], 55)
+    before = [x.clone() for x in (cache.mass, cache.seq_lens, cache.block_tables)]
+    for keep in (2 ** 32, 2 ** 63 - 1):
+        with pytest.raises(ValueError, match="keep_tiles"):
+            cache.evict(keep, 0, 0)
+    with pytest.raises(ValueError, match="sink_tiles"):
+        cache.evict(2, 2 ** 32, 0)
+    q = rows(cfg, 2, 56)[0]
+    args = [cfg, q, torch.empty_like(q), cache.mass, cache.seq_lens, cache.block_tables, cache.k_pool, cache.v_pool,
+            cache.k_tail, cache.v_tail, cache.workspace]
+    for at, small in ((6, cache.k_pool[:-1]), (7, cache.v_pool[:-1]), (8, cache.k_tail[:1]), (9, cache.v_tail[:, :1])):
+        with pytest.raises(ValueError):
+            kvq.paged_decode_attention_mass(*args[:at], small, *args[at + 1:], num_blocks=cache.num_blocks)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(before, (cache.mass, cache.seq_lens, cache.block_tables)))
+
+
 @pytest.mark.parametrize("lens", [[0, 0], [5, 0], [0, 64]], ids=str)
 def test_prompts_without_tokens_or_tiles(lens):
     cfg = config()
