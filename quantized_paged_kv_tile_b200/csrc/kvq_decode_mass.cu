@@ -9,6 +9,7 @@
 // are 8 bytes per (tile, query head) against the tile's 9216 bytes per KV head
 // (T = 64, 4-bit codes).
 #include "kvq_decode_kernel.cuh"
+#include "kvq_launch.cuh"
 
 namespace kvq {
 
@@ -29,6 +30,7 @@ constexpr int kMassWarps = 4;
 __global__ void __launch_bounds__(kMassWarps * 32) decode_mass_kernel(DecodeArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.y, T = a.cfg.tile_tokens, hqn = a.cfg.num_kv_heads * a.cfg.group_size;
+  cudaGridDependencySynchronize();
   const int tiles = (max(a.seq_lens[b], 0) + T - 1) / T;
   const int served = min(tiles, min(a.mass_tiles, a.mass_stat_tiles));
   if (blockIdx.x == 0 && threadIdx.x == 0 && served < tiles) report_error(a.dev_status, KVQ_ERR_DEVICE_BOUNDS);
@@ -98,8 +100,7 @@ cudaError_t launch_paged_decode_mass(DecodeArgs a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int per_cta = kMassTilesPerWarp * kMassWarps;
   const int tiles = std::min(a.mass_tiles, a.mass_stat_tiles);
-  decode_mass_kernel<<<dim3((tiles + per_cta - 1) / per_cta, a.num_seqs), kMassWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_behind(decode_mass_kernel, dim3((tiles + per_cta - 1) / per_cta, a.num_seqs), kMassWarps * 32, s, a);
 }
 
 }  // namespace kvq

@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "kvq_device.cuh"
+#include "kvq_launch.cuh"
 #include "kvq_sm100.cuh"
 
 namespace kvq {
@@ -1080,6 +1081,7 @@ __global__ void __launch_bounds__(kMassWarps * 32) prompt_mass_kernel(PromptDev 
   const int e = blockIdx.x * 32 + lane;
   Unit u{static_cast<int>(blockIdx.y), 0, 0, 0, 0};
   u.n = seq_len(a, u.seq, u.first);
+  cudaGridDependencySynchronize();
   if (blockIdx.x * 32 * wid >= u.n) return;
   const int w0 = a.mass_window == 0 ? 0 : max(0, u.n - a.mass_window) / W1;
   const int rows = ((u.n + W1 - 1) / W1 - w0) * nh;  // from query tile w0 on
@@ -1217,8 +1219,8 @@ cudaError_t launch_prompt(const PromptArgs& a, cudaStream_t s) {
     e = launch_prompt_kernel<D, MASS, false>(mq, mk, mv, pd, z.grid, s);
   if (e != cudaSuccess || !MASS) return e;
   const int wid = std::min(a.cfg.tile_tokens, Geo::kKeys);
-  prompt_mass_kernel<<<dim3((a.max_seq_tokens + 32 * wid - 1) / (32 * wid), a.num_seqs), kMassWarps * 32, 0, s>>>(pd, Geo::kKeys);
-  return cudaGetLastError();
+  return launch_behind(prompt_mass_kernel, dim3((a.max_seq_tokens + 32 * wid - 1) / (32 * wid), a.num_seqs),
+                       kMassWarps * 32, s, pd, static_cast<int>(Geo::kKeys));
 }
 
 // ------------------------------------------------------------------ self-test
