@@ -23,8 +23,9 @@
 //   softmax warps  (four per stream, a row per thread) S from TMEM, running
 //                  maximum and sum in registers, P as fp16 to TMEM, O rescaled
 //                  where the maximum moved far; at the end O / l to memory
-// P is rounded to fp16 (half a step is 2^-11 of each weight; the sum l takes
-// the unrounded weights), everything else stays in fp32.
+// P is rounded to fp16 (half a step is 2^-11 of each weight, or 2^-25 of the
+// row's largest for those below 2^-14 of it; the sum l takes the unrounded
+// weights), everything else stays in fp32.
 //
 // What bounds it: at d = 128 a pair of 128 x 128 tiles needs 2048 cycles of
 // the tensor pipe and 2186 of the exponential unit (measured: 128 exponentials
@@ -32,7 +33,7 @@
 // chain P -> P V -> Q K^T -> S -> maximum -> exponentials of a query tile; long
 // calls run into the power limit first (1567 MHz at 1000 W; a library fp16
 // GEMM of 8192^3 settles at 1287 TFLOP/s there, this kernel at 1050: 16384
-// tokens x 64 heads in 4.18 ms, 1218 TFLOP/s in short runs).  Replacing 1/8 to
+// tokens x 64 heads in 4.16 to 4.27 ms, 1218 TFLOP/s in short runs).  Replacing 1/8 to
 // 3/8 of the exponentials by a polynomial on the FMA pipe gained 1.6% on short
 // runs and lost 4 to 11% on long ones.
 //

@@ -70,6 +70,11 @@ def definition(cfg, q, k, v, lens, window=0, scale=None, starts=None):
                 eps = d * U32 * size + 16 * U32 + U32 * lse[at:at + n, h].abs()
                 worst = max(worst, float(eps.max()))
                 e_out[at:at + n, h] = (U16 + 2 * eps)[:, None] * (p @ vv.abs()) + U16 * out[at:at + n, h].abs() + 2.0 ** -24
+                # a weight below 2^-14 of the row's largest is rounded as a
+                # subnormal fp16, to a multiple of 2^-24: off by half of that
+                # (the maximum it is relative to is never above the row's)
+                top = p.amax(1, keepdim=True)
+                e_out[at:at + n, h] += 2.0 ** -25 * top * (((p < 1.01 * 2.0 ** -14 * top) & see).double() @ vv.abs())
                 e_lse[at:at + n, h] = 2 * eps + 4 * U32 * lse[at:at + n, h].abs()
                 counted = p[max(0, n - window) if window else 0:].sum(0)
                 mass[s].index_add_(0, torch.arange(n, device="cuda") // t, counted)
