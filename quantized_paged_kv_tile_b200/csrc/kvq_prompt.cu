@@ -1037,8 +1037,16 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           // across the lanes this took 3.8 us a unit), then the lanes by butterfly
           const float4 f = *reinterpret_cast<const float4*>(s_m + 4 * lane);
           const float4 w = *reinterpret_cast<const float4*>(s_w + 4 * lane);
-          // a row that does not count has weight 0, and its sums may be anything
-          auto term = [](float x, float y, float f, float w) { return w != 0.f ? x * ex2(y - f) * w : 0.f; };
+          // A row that does not count has weight 0, and its sums may be
+          // anything.  An entry that a row does not see is none of its
+          // weight, whatever the row is.  A share without a finite score is
+          // relative to 0 and not to a maximum, which may lie above f.
+          int sees[4];  // tokens of this lane's rows
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sees[r] = first + (4 * lane + r) / G;
+          auto term = [](float x, float y, float f, float w, bool seen) {
+            return w != 0.f && seen ? x * ex2(fminf(y - f, 0.f)) * w : 0.f;
+          };
           const int stride = (ent + 1) * kRows, ent_bits = ent == 4 ? 2 : ent - 1;
           const int entries = (SPLIT ? (min(u.n, first + W1) + KT - 1) / KT : nk) * ent;
 #pragma unroll 4
@@ -1046,8 +1054,10 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             const float* tile = base + static_cast<size_t>(i >> ent_bits) * stride + 4 * lane;
             const float4 x = *reinterpret_cast<const float4*>(tile + (i & (ent - 1)) * kRows);
             const float4 y = *reinterpret_cast<const float4*>(tile + ent * kRows);
-            const float sum = warp_sum((term(x.x, y.x, f.x, w.x) + term(x.y, y.y, f.y, w.y)) +
-                                       (term(x.z, y.z, f.z, w.z) + term(x.w, y.w, f.w, w.w)));
+            const int key = i * wid;  // the entry's first
+            const float sum =
+                warp_sum((term(x.x, y.x, f.x, w.x, sees[0] >= key) + term(x.y, y.y, f.y, w.y, sees[1] >= key)) +
+                         (term(x.z, y.z, f.z, w.z, sees[2] >= key) + term(x.w, y.w, f.w, w.w, sees[3] >= key)));
             if (lane == 0) dst[i] = sum;
           }
           asm volatile("bar.sync %0, 128;" ::"r"(1 + q) : "memory");
