@@ -462,7 +462,9 @@ KVQ_API kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seq
  *                  131072 tokens, 8 KV heads, g = 8, T = 64), with a window
  *                  with max_seq_tokens.
  * A row that sees a NaN, or an infinite score, gives NaN, one that sees an
- * infinite value gives infinity or NaN there; values that a row does not see
+ * infinite value gives infinity or NaN there.  Scores (q.k * softmax_scale) of
+ * 1.16e7 (2^24 log2 units) and more in magnitude, whose fp32 numbers have no
+ * fraction left, count as infinite of their sign.  Values that a row does not see
  * (later tokens, other sequences, rows behind the last one) never reach it,
  * whatever they are.  A sequence whose prefix sums are negative,
  * descending, past total_tokens or longer than max_seq_tokens is skipped and

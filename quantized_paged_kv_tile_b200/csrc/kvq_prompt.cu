@@ -75,6 +75,12 @@ constexpr int kRows = 128;    // query rows per query tile (TMEM lanes)
 // keys of very different channel stds (scores spread over some 30 units) a
 // limit of 8 took 4853 us on 16384 tokens x 64 heads.
 constexpr float kLazy = 15.f;
+// Scaled scores (log2 units) from here on count as infinite, those below the
+// negative as -inf.  The exponent's multiply-add rounds once, the scaled
+// maximum that it subtracts before: up to here by half a unit at most, all of a
+// row's weights alike, which l cancels; further out that would take them out of
+// fp16's range.  (A score has no bits below one left there.)
+constexpr float kFar = 16777216.f;  // 2^24
 // up to this many sequences the units are taken longest first
 constexpr int kSortedSeqs = 1024;
 
@@ -784,15 +790,16 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
             for (int k = 0; k < 4; ++k) mx[k] = max3nan(mx[k], s[c + k], s[c + 4 + k]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mx[k] = max3nan(mx[k], s[e - 4 + k], s[e - 4 + k]);
-          const float t = max3nan(mx[0], mx[1], max3nan(mx[2], mx[3], mx[3])) * pd.qscale;
-          if (!(t < INFINITY)) l = NAN;  // a NaN or an infinite score: the row is NaN
+          // (rounded as it is kept, not again inside a multiply-add)
+          const float t = __fmul_rn(max3nan(mx[0], mx[1], max3nan(mx[2], mx[3], mx[3])), pd.qscale);
+          if (!(t < kFar)) l = NAN;  // a NaN or an infinite score: the row is NaN
           return t;
         };
         // The maximum moves to `top` in the lanes where it is more than kLazy
         // larger (m = -inf before the first finite score); O and l follow.
         auto grow = [&](float top) {
           float alpha = 1.f;
-          if (top > m + kLazy) {
+          if (top > m + kLazy && top > -kFar) {
             alpha = ex2(m - top);
             m = top;
             l *= alpha;

@@ -7,7 +7,7 @@ import torch
 
 from quantized_paged_kv_tile_b200 import build, kvq
 
-from test_gpu_prompt import call, check, config, rows
+from test_gpu_prompt import U16, U32, call, check, config, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,102 @@ def test_a_nan_row_stays_out_of_the_tiles_it_does_not_see(d):
     assert bool(torch.isnan(mass[0, 0]))
     # the tiles behind it: bit for bit, the row had no weight there
     assert torch.equal(mass[0, 1:], want[0, 1:]) and torch.equal(mass[1], want[1])
+
+
+# ------------------------------------------------------------------ large scores
+def one_channel(cfg, n, q0, k0, seed):
+    """Rows whose scores are the products of their first channels: exact in fp32."""
+    q, k, v = rows(cfg, n, seed)
+    q.zero_()
+    k.zero_()
+    q[..., 0] = q0
+    k[..., 0] = k0
+    return q, k, v
+
+
+@pytest.mark.parametrize("n,hkv", [(300, 1), (700, 40)])
+@pytest.mark.parametrize("q0,k0", [(2048.0, 4096.0), (2048.0, -4096.0), (-3000.0, -3500.0), (64.0, -4096.0)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_equal_scores_of_any_size(d, q0, k0, n, hkv):
+    """All scores of a row are the same number, up to 1.05e7: the weights are 1 / (i + 1)."""
+    cfg = config(hkv, 2, d)
+    q, k, v = one_channel(cfg, n, q0, k0, 33)
+    out, lse, mass, status = call(cfg, q, k, v, [n], 0, scale=1.0)
+    assert status == 0
+    count = torch.arange(1, n + 1, device="cuda", dtype=torch.float64)[:, None, None]
+    mean = v.double().cumsum(0).div(count).repeat_interleave(2, 1)
+    size = v.double().abs().cumsum(0).div(count).repeat_interleave(2, 1)
+    # equal weights are rounded alike, to at worst 2^-11 of them; the sums and the quotient in fp32
+    bound = (U16 + (n + 16) * U32) * size + U16 * mean.abs() + 2.0 ** -24
+    assert bool(((out.double() - mean).abs() <= bound).all())
+    score = q0 * k0
+    assert bool(((lse.double() - score).abs() <= math.log(n) + 8 * U32 * abs(score)).all())
+    # row i gives 1 / (i + 1) to each token it sees, from every query head
+    share = (1.0 / count[:, 0, 0]).flip(0).cumsum(0).flip(0) * cfg.num_q_heads
+    tiles = torch.zeros(mass.shape[1], dtype=torch.float64, device="cuda")
+    tiles.index_add_(0, torch.arange(n, device="cuda") // cfg.tile_tokens, share)
+    assert bool(((mass[0].double() - tiles).abs() <= 4096 * U32 * tiles).all())
+
+
+@pytest.mark.parametrize("base", [0.0, 2048.0, -2048.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_weights_relative_to_a_large_maximum(d, base):
+    """Scores of 2^22 + whole numbers that rise by 0 to 3 a key: the weights
+    depend on the differences alone, also where the maximum moves."""
+    cfg = config(1, 4, d)
+    n = 400
+    q, k, v = one_channel(cfg, n, 2048.0, base, 34)
+    rise = torch.randint(0, 4, (n,), generator=torch.Generator().manual_seed(35)).cumsum(0)
+    q[..., 1] = 1.0
+    k[..., 1] = rise.cuda().half()[:, None]
+    assert int(rise[-1]) < 2048
+    out, _, _, status = call(cfg, q, k, v, [n], scale=math.log(2.0))
+    assert status == 0
+    see = torch.ones((n, n), dtype=torch.bool, device="cuda").tril()
+    x = (rise.double().cuda()[None, :] * (math.log(2.0) * math.log2(math.e))).expand(n, n).masked_fill(~see, -math.inf)
+    p = torch.softmax(x * math.log(2.0), 1)
+    want, size = p @ v[:, 0].double(), p @ v[:, 0].double().abs()
+    # weights and output rounded to fp16; an exponent of up to 30 in fp32; small weights to a multiple of 2^-24
+    bound = (U16 + 64 * U32) * size + U16 * want.abs() + 2.0 ** -24
+    top = p.amax(1, keepdim=True)
+    bound += 2.0 ** -25 * top * (((p < 1.01 * 2.0 ** -14 * top) & see).double() @ v[:, 0].double().abs())
+    for h in range(4):
+        assert bool(((out[:, h].double() - want).abs() <= bound).all())
+
+
+def hidden_keys(d, q0, k0):
+    """Keys whose scores are q0 x k0, minus infinity or as good as that, weigh
+    nothing; rows that see no other key are NaN."""
+    cfg = config(1, 3, d, t=32)
+    n = 300
+    q, k, v = rows(cfg, n, 37)
+    q[..., 0], k[..., 0] = q0, 0.0
+    hidden = torch.zeros(n, dtype=torch.bool)
+    hidden[:5] = True
+    hidden[[40, 128, 129, 200]] = True
+    kk = k[:, 0].double()
+    k[hidden.cuda(), :, 0] = k0
+    out, lse, mass, status = call(cfg, q, k, v, [n], 0)
+    assert status == 0
+    assert bool(torch.isnan(out[:5]).all())
+    see = torch.ones((n, n), dtype=torch.bool, device="cuda").tril() & (~hidden).cuda()
+    for h in range(3):
+        qq = q[:, h].double()
+        x = (qq @ kk.T * d ** -0.5).masked_fill(~see, -math.inf)[5:]
+        p = torch.softmax(x, 1)
+        size = (qq[:, 1:].abs() @ kk[:, 1:].abs().T * d ** -0.5).amax()
+        eps = float(d * U32 * size + 16 * U32)
+        want, absolute = p @ v[:, 0].double(), p @ v[:, 0].double().abs()
+        bound = (U16 + 2 * eps) * absolute + U16 * want.abs() + n * 2.0 ** -25 * v.double().abs().amax() + 2.0 ** -24
+        assert bool(((out[5:, h].double() - want).abs() <= bound).all())
+        ref = torch.logsumexp(x, 1)
+        assert bool(((lse[5:, h].double() - ref).abs() <= 2 * eps + 4 * U32 * ref.abs()).all())
+    return cfg, q, k, v, out
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scores_past_the_limit_count_as_infinite(d):
+    cfg, q, k, v, want = hidden_keys(d, 32768.0, -32768.0)
+    k[250, 0, 0] = 32768.0  # a score of 2^30 and more
+    out = call(cfg, q, k, v, [300])[0]
+    assert bool(torch.isnan(out[250:]).all()) and torch.equal(out[5:250], want[5:250])
