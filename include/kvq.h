@@ -429,7 +429,8 @@ KVQ_API kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seq
  * beside) their quantization into an empty cache.  Token i of sequence s
  * (query head j, reading KV head j / group_size) attends to tokens 0..i of
  * its sequence: softmax(q.k * softmax_scale) V, statistics and sums in fp32,
- * the weights rounded to fp16 for the product with V.
+ * the weights rounded to fp16 for the product with V: by 2^-11 of each, and
+ * very small ones by what sums to less than 2^-12 of the row's largest weight.
  *   q            : device fp16, total_tokens rows of [num_kv_heads*group_size][d],
  *                  q_stride elements from row to row; not rotated.
  *   k, v         : device fp16, total_tokens rows of [num_kv_heads][d], k_stride

@@ -23,9 +23,10 @@
 //   softmax warps  (four per stream, a row per thread) S from TMEM, running
 //                  maximum and sum in registers, P as fp16 to TMEM, O rescaled
 //                  where the maximum moved far; at the end O / l to memory
-// P is rounded to fp16 (half a step is 2^-11 of each weight, or 2^-25 of the
-// row's largest for those below 2^-14 of it; the sum l takes the unrounded
-// weights), everything else stays in fp32.
+// P is rounded to fp16 (half a step is 2^-11 of each weight; for those below
+// 2^-14 of the row's largest 2^-25 of that, or less where the keys are many, see
+// spare_bits; the sum l takes the unrounded weights), everything else stays in
+// fp32.
 //
 // What bounds it: at d = 128 a pair of 128 x 128 tiles needs 2048 cycles of
 // the tensor pipe and 2186 of the exponential unit (measured: 128 exponentials
@@ -81,6 +82,15 @@ constexpr float kLazy = 15.f;
 // row's weights alike, which l cancels; further out that would take them out of
 // fp16's range.  (A score has no bits below one left there.)
 constexpr float kFar = 16777216.f;  // 2^24
+// When the maximum moves, a weight of 2^spare goes to the score it moves to, so
+// that small weights are rounded as late.  A weight is rounded to a multiple of
+// fp16's smallest, 2^-24, at worst: off by 2^-25 of 2^-spare of the row's
+// largest, and over `keys` keys by less than 2^-12 of it (half a step of an
+// fp16 output is 2^-12 to 2^-11 of that).  Every bit spared leaves kLazy one
+// less: up to 8192 keys none is needed, 2 at 32768, 7 at 2^20 (us without and
+// with, spread scores: 16384 tokens x 64 heads 3838 / 3899, 131072 x 4 14990 /
+// 15280; d = 64, 32768 x 16: 2886 / 2881).
+__device__ __forceinline__ float spare_bits(int keys) { return static_cast<float>(max(0, 19 - __clz(keys - 1))); }
 // up to this many sequences the units are taken longest first
 constexpr int kSortedSeqs = 1024;
 
@@ -768,6 +778,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       // tiles that both streams have: they take turns
       const int turns = !Geo::kTurns ? 0 : min(nk, stream_work<KT, SPLIT>(u.run * W1 * UQ, 1 - q, W1, u.n).count());
       float m = -INFINITY, l = 0.f;
+      const float spare = spare_bits(min(u.n, first + W1));
       bool ok = true;
       for (int step = 0; step < nk; ++step) {
         const int j = w.lo + step;  // key tile
@@ -800,8 +811,9 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
         auto grow = [&](float top) {
           float alpha = 1.f;
           if (top > m + kLazy && top > -kFar) {
-            alpha = ex2(m - top);
-            m = top;
+            const float to = top - spare;
+            alpha = ex2(m - to);
+            m = to;
             l *= alpha;
           }
           if (step == 0) return;

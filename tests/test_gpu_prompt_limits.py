@@ -146,3 +146,29 @@ def test_scores_past_the_limit_count_as_infinite(d):
     k[250, 0, 0] = 32768.0  # a score of 2^30 and more
     out = call(cfg, q, k, v, [300])[0]
     assert bool(torch.isnan(out[250:]).all()) and torch.equal(out[5:250], want[5:250])
+
+
+# ------------------------------------------------------------------ long flat tails
+@pytest.mark.parametrize("d,n,hkv", [(64, 1 << 20, 1), (128, 200000, 1), (256, 100000, 1), (128, 30000, 1),
+                                     (64, 32768, 1), (128, 20000, 8)])
+def test_a_long_flat_tail_keeps_its_weight(d, n, hkv):
+    """One key far above all others, every other weight 2^-25.5 of its own.
+    A weight rounded to fp16 is off by at most half a step, 2^-25 of 2^-b of
+    the row's largest for the smallest ones, with b = ceil(log2 keys) - 13 >= 0:
+    over all keys at most 2^-12 of the largest value's size."""
+    cfg = config(hkv, 1, d)
+    q, k, v = one_channel(cfg, n, 1.0, -17.6875, 36)
+    k[0] = 0.0
+    v.fill_(1.0)
+    v[0] = 0.0
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out = torch.full(q.shape, 7.0, dtype=torch.float16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.prompt_attention(cfg, q, k, v, out, cu, n, softmax_scale=1.0, dev_status=status)
+    tail = torch.arange(n, device="cuda", dtype=torch.float64) * math.exp(-17.6875)
+    want = (tail / (1.0 + tail))[:, None]
+    # the weights' relative error, and the sums': n terms in fp32
+    bound = 2.0 ** -12 + (2 * U16 + 64 * U32) * want + 2.0 ** -24
+    assert int(status) == 0
+    for h in range(hkv):
+        assert bool(((out[:, h].double() - want).abs() <= bound).all()), float((out[:, h].double() - want).abs().max())
