@@ -467,10 +467,11 @@ KVQ_API kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seq
  * 1.16e7 (2^24 log2 units) and more in magnitude, whose fp32 numbers have no
  * fraction left, count as infinite of their sign.  Values that a row does not see
  * (later tokens, other sequences, rows behind the last one) never reach it,
- * whatever they are.  A sequence whose prefix sums are negative,
- * descending, past total_tokens or longer than max_seq_tokens is skipped and
- * reported through dev_status (KVQ_ERR_DEVICE_BOUNDS).  All pointers 16-byte
- * aligned; the call is asynchronous on stream. */
+ * whatever they are.  A sequence whose prefix sums are negative, past
+ * total_tokens or longer than max_seq_tokens is skipped, and where they descend
+ * that sequence and all behind it are; either is reported through dev_status
+ * (KVQ_ERR_DEVICE_BOUNDS).  All pointers 16-byte aligned; the call is
+ * asynchronous on stream. */
 KVQ_API kvq_status kvq_prompt_attention(const kvq_config* cfg, const void* q, int q_stride, const void* k,
                                         int k_stride, const void* v, int v_stride, void* out, float* lse,
                                         const int32_t* cu_seqlens, int num_seqs, int total_tokens,

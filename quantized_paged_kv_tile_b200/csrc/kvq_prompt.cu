@@ -122,7 +122,9 @@ struct Unit {
   int seq, run, head, n, first;  // n = 0: nothing here
 };
 
-// Finds the units; one warp uses it, all lanes together.
+// Finds the units; one warp uses it, all lanes together.  Only sequences before
+// the first descent of the prefix sums have any: behind it they could overlap
+// earlier ones, and the units would be more than the host counted.
 // Up to kSortedSeqs sequences: units in descending order of their run index
 // (so of their keys), from a binary search over the levels, count(c) = number
 // of runs >= c.  Up to 32 sequences their run counts stay in registers, a lane
@@ -133,10 +135,17 @@ class UnitFinder {
  public:
   // (the numbers are copied: read through a reference to the kernel's
   // arguments each cost a trip through memory)
-  __device__ UnitFinder(const PromptDev& pd, int lane)
+  // `ascending`: sequences before the first descent, where there are more than 32
+  __device__ UnitFinder(const PromptDev& pd, int ascending, int lane)
       : cu_(pd.a.cu_seqlens), seqs_(pd.a.num_seqs), total_(pd.a.total_tokens), longest_(pd.a.max_seq_tokens),
         heads_(pd.a.cfg.num_kv_heads), W_(pd.unit_tokens), magic_(pd.unit_magic), lane_(lane) {
     int f;
+    if (seqs_ > 32) {
+      seqs_ = ascending;
+    } else {
+      const unsigned down = __ballot_sync(kFull, lane < seqs_ && cu_[lane + 1] < cu_[lane]);
+      if (down != 0) seqs_ = __ffs(down) - 1;
+    }
     if (lane < seqs_) mine_ = runs(len(lane, f));
   }
 
@@ -293,6 +302,7 @@ struct Shared {  // at Geom::kMisc
   uint32_t tmem;
   int stop;
   int edges, guarded;     // edge tiles, in all, whose V is on its way / that the V guard is done with
+  int ascending;          // more than 32 sequences: those before the first descent of the prefix sums
   int odd_v[kUnitSlots];  // per unit: V values of an edge tile were left out
   Unit unit[kUnitSlots];
 };
@@ -372,6 +382,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
   auto bar = [&](int i) { return bars + 8 * i; };
   Shared* sh = reinterpret_cast<Shared*>(smem + Geo::kMisc);
   volatile int* stop = &sh->stop;
+  auto ascending = [&] { return a.num_seqs > 32 ? sh->ascending : a.num_seqs; };
 
   // rows of the Q tiles that no box fills (g not a divisor of 128) stay zero
   if (kRows % G != 0) {
@@ -404,6 +415,13 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
     mbar_init_fence();
     sh->stop = 0;
     sh->edges = sh->guarded = 0;
+    sh->ascending = a.num_seqs;
+  }
+  if (a.num_seqs > 32) {
+    __syncthreads();
+    for (int s = tid; s < a.num_seqs; s += Geo::kThreads)
+      if (a.cu_seqlens[s + 1] < a.cu_seqlens[s]) atomicMin(&sh->ascending, s);
+    __syncthreads();
   }
   if (warp == 0) tmem_alloc512(smem_u32(&sh->tmem));
   // the last warp looks up the first unit meanwhile
@@ -414,7 +432,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       tma_prefetch_map(&mk);
       tma_prefetch_map(&mv);
     }
-    if (blockIdx.x < pd.units) first_unit = UnitFinder(pd, lane).find(blockIdx.x);
+    if (blockIdx.x < pd.units) first_unit = UnitFinder(pd, ascending(), lane).find(blockIdx.x);
     if (first_unit.n == 0 && a.num_seqs <= kSortedSeqs) first_unit.n = -1;
   }
   fence_before();
@@ -642,7 +660,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
       // Units of this CTA: every gridDim.x-th, in alternating direction (with
       // units longest first the CTAs end up with about the same work).
       Ring pub, ru, ring[2] = {{0}, {SPLIT ? KS : 0}};
-      const UnitFinder finder(pd, lane);
+      const UnitFinder finder(pd, ascending(), lane);
       int round = 1;
       bool more = true;
       auto publish = [&](Unit u) {  // the next unit from u on, n = -1 after the last
@@ -1111,8 +1129,13 @@ __global__ void __launch_bounds__(kMassWarps * 32) prompt_mass_kernel(PromptDev 
   const int e = blockIdx.x * 32 + lane;
   Unit u{static_cast<int>(blockIdx.y), 0, 0, 0, 0};
   u.n = seq_len(a, u.seq, u.first);
+  bool down = false;  // behind a descent of the prefix sums
+  if (u.seq > 0) {
+    for (int s = threadIdx.x; s < u.seq; s += kMassWarps * 32) down |= a.cu_seqlens[s + 1] < a.cu_seqlens[s];
+    down = __syncthreads_or(down);
+  }
   cudaGridDependencySynchronize();
-  if (blockIdx.x * 32 * wid >= u.n) return;
+  if (down || blockIdx.x * 32 * wid >= u.n) return;
   const int w0 = a.mass_window == 0 ? 0 : max(0, u.n - a.mass_window) / W1;
   const int rows = ((u.n + W1 - 1) / W1 - w0) * nh;  // from query tile w0 on
   // the first row that sees the entry (rows before it may not have written it)

@@ -2,6 +2,7 @@
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -172,3 +173,28 @@ def test_a_long_flat_tail_keeps_its_weight(d, n, hkv):
     assert int(status) == 0
     for h in range(hkv):
         assert bool(((out[:, h].double() - want).abs() <= bound).all()), float((out[:, h].double() - want).abs().max())
+
+
+# ------------------------------------------------------------------ prefix sums that descend
+@pytest.mark.parametrize("before", [0, 40, 1100])
+def test_sequences_from_a_descent_on_are_skipped(before):
+    """Prefix sums that go back and forth over the same rows: the sequences
+    before the descent keep their results (masses too), those from it on are
+    skipped, and the call reports it.  `before`: sequences of one token ahead."""
+    cfg = config(8, 8)
+    n = before + 1000
+    q, k, v = rows(cfg, n, 38)
+    good = [1] * before + [600, 400]
+    want, want_lse, want_mass, status = call(cfg, q, k, v, good, 0)
+    assert status == 0
+    cu = list(np.concatenate([[0], np.cumsum(good)])) + [before, n, before + 500]
+    for window in (0, 100):
+        out, lse, mass, status = call(cfg, q, k, v, good, window, cu=cu, max_len=1000)
+        assert status == kvq.KVQ_ERR_DEVICE_BOUNDS
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert bool((mass[len(good):] == 0).all())
+        if window == 0:
+            assert torch.equal(mass[:len(good), :want_mass.shape[1]], want_mass)
+            assert bool((mass[:, want_mass.shape[1]:] == 0).all())
+    out = call(cfg, q, k, v, [n], 0, cu=[n, 0, n], max_len=n)[0]  # nothing before the descent
+    assert bool((out == 7.0).all())
