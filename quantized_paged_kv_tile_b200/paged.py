@@ -313,8 +313,11 @@ class DecodeStepGraph:
         self.out = torch.empty_like(self.q)
         self._cu = torch.arange(b + 1, dtype=torch.int32, device=dev)
         need = cache._decode_bytes(self.num_splits)
-        if cache.workspace.numel() < need:
-            cache.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        # the graph holds the buffer whose address it records; the cache's stays
+        # the cache's, other graphs may have recorded it
+        self.workspace = cache.workspace
+        if self.workspace.numel() < need:
+            self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         # the fused step's own workspace: zero-filled once, left zero by every step
         self.step_workspace = torch.zeros(need, dtype=torch.uint8, device=dev) if fused else None
         self.graph = torch.cuda.CUDAGraph()
@@ -335,7 +338,7 @@ class DecodeStepGraph:
                 self._fused_step()
 
     def _decode(self, mass) -> None:
-        self.cache._run_decode(self.q, self.out, self.cache.workspace, self.num_splits, mass)
+        self.cache._run_decode(self.q, self.out, self.workspace, self.num_splits, mass)
 
     def _step(self) -> None:
         c = self.cache
