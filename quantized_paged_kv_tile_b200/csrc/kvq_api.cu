@@ -1,5 +1,7 @@
 // C ABI of the library: argument validation on the host, then the kernel
 // launchers.  See include/kvq.h for the contract of every entry point.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdarg>
@@ -148,12 +150,40 @@ kvq_status check_row_stride(int stride, int row, const char* name) {
 }  // namespace
 
 cudaError_t kvq::device_sm_count(int* sms) {
-  static PerDevice known;
-  return known.get(sms, [](int* v) {
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    return e != cudaSuccess ? e : cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev);
-  });
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices] = {};  // 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < kDevices;
+  if (kept && (*sms = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && kept) known[dev].store(*sms, std::memory_order_release);
+  return e;
+}
+
+unsigned long long kvq::current_context_id() {
+  struct Driver {
+    PFN_cuCtxGetCurrent_v4000 current = nullptr;
+    PFN_cuCtxGetId_v12000 id = nullptr;
+    Driver() {
+      void* p = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      auto look_up = [&](const char* name) {
+        return cudaGetDriverEntryPoint(name, &p, cudaEnableDefault, &q) == cudaSuccess &&
+               q == cudaDriverEntryPointSuccess;
+      };
+      if (look_up("cuCtxGetCurrent")) current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
+      if (look_up("cuCtxGetId")) id = reinterpret_cast<PFN_cuCtxGetId_v12000>(p);
+    }
+  };
+  static const Driver driver;
+  CUcontext c = nullptr;
+  unsigned long long id = 0;
+  if (driver.current == nullptr || driver.id == nullptr || driver.current(&c) != CUDA_SUCCESS || c == nullptr ||
+      driver.id(c, &id) != CUDA_SUCCESS)
+    return 0;
+  return id;
 }
 
 extern "C" {

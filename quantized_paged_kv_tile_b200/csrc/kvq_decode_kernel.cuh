@@ -1282,7 +1282,7 @@ int device_sms() {
 template <int T, int BK, int BV, bool MASS>
 cudaError_t decode_ctas_per_sm(int* per_sm) {
   using Geo = DecodeGeom<T, BK, BV>;
-  static PerDevice known;
+  static PerContext<int> known;
   return known.get(per_sm, [](int* v) {
     auto kern = decode_tiles_kernel<T, BK, BV, MASS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo::kSmem);

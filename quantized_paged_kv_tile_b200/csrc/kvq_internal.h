@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "../../include/kvq.h"
 
@@ -30,31 +31,48 @@ struct PoolGeom {
 
 PoolGeom pool_geom(const kvq_config& cfg, bool is_v);
 
-// A number that one device and kernel instance fix, asked for once per device
-// (ordinals past the table are asked for every time).  The set-up of a launch
-// (shared-memory opt-in, occupancy) costs the host 1 to 4 us a call otherwise.
-class PerDevice {
+// SMs of the current device (asked for once per device)
+cudaError_t device_sm_count(int* sms);
+
+// Id of the current context, unique for the life of the process; 0: none yet.
+unsigned long long current_context_id();
+
+// What the set-up of a kernel instance gives (shared-memory opt-in, occupancy),
+// asked for once per context, which is what the opt-in belongs to: a reset
+// device and a second context of a device start without it.  Asked for on every
+// call it costs the host 1 to 4 us.
+template <class V>
+class PerContext {
  public:
-  // f(int* value) -> cudaError_t
+  // f(V* value) -> cudaError_t
   template <class F>
-  cudaError_t get(int* value, F&& f) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool kept = dev >= 0 && dev < kDevices;
-    if (kept && (*value = known_[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
-    e = f(value);
-    if (e == cudaSuccess && kept) known_[dev].store(*value, std::memory_order_release);
+  cudaError_t get(V* value, F&& f) {
+    const unsigned long long id = current_context_id();
+    const std::lock_guard<std::mutex> lock(mutex_);
+    if (id != 0)
+      for (const Known& k : known_)
+        if (k.id == id) {
+          *value = k.value;
+          return cudaSuccess;
+        }
+    const cudaError_t e = f(value);
+    if (e == cudaSuccess && id != 0) {
+      known_[next_] = {id, *value};
+      next_ = (next_ + 1) % kContexts;
+    }
     return e;
   }
 
  private:
-  static constexpr int kDevices = 64;
-  std::atomic<int> known_[kDevices] = {};  // 0: not asked yet
+  struct Known {
+    unsigned long long id;  // 0: free
+    V value;
+  };
+  static constexpr int kContexts = 64;
+  std::mutex mutex_;
+  Known known_[kContexts] = {};
+  int next_ = 0;  // the entry to be given up next
 };
-
-// SMs of the current device
-cudaError_t device_sm_count(int* sms);
 
 // Quantize work: one item per (tile, head, K/V).
 struct QuantizeArgs {

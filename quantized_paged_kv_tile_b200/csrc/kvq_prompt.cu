@@ -1229,7 +1229,7 @@ template <int D, bool MASS, bool SPLIT>
 cudaError_t launch_prompt_kernel(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                                  const PromptDev& pd, int grid, cudaStream_t s) {
   using Geo = Geom<D, MASS>;
-  static PerDevice opted_in;  // to the shared memory, once per device
+  static PerContext<int> opted_in;  // to the shared memory
   auto kern = prompt_kernel<D, MASS, SPLIT>;
   int done = 0;
   const cudaError_t e = opted_in.get(&done, [&](int* v) {
