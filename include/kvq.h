@@ -98,7 +98,8 @@
  *    device code, so every device that loads the library's module (at its
  *    first kernel launch, or at start-up with CUDA_MODULE_LOADING=EAGER)
  *    holds those 32 MiB until the process exits, whether or not that entry
- *    point is ever called; plus that array's address per device.
+ *    point is ever called; plus that array's address, and what the set-up of
+ *    each kernel gave, per CUDA context.
  *  - Every call is asynchronous on `stream` (0 = legacy default stream) and
  *    never synchronizes.  Arguments are validated on the host first; an
  *    invalid call returns an error and launches nothing.
@@ -403,12 +404,9 @@ KVQ_API kvq_status kvq_paged_prefill_attention(const kvq_config* cfg, const void
  *   exceeds KVQ_DECODE_STATIC_SCRATCH_BYTES the call returns
  *   KVQ_ERR_WORKSPACE (detail in kvq_last_error) before touching the device;
  *   use fewer sequences per call, a smaller num_splits, or the workspace entry.
- *   Set-up: the first call on each device (that device current) looks up the
- *   array's address with cudaGetSymbolAddress and keeps it; make that first
- *   call before any stream capture begins.  Device ordinals 0..63.  The kept
- *   address belongs to the device's current context: after cudaDeviceReset
- *   (or any destruction of the primary context) the array may move, so do not
- *   call this entry point again in that process after a reset.
+ *   Set-up: the first call in each CUDA context (that context current) looks up
+ *   the array's address with cudaGetSymbolAddress and keeps it; make that first
+ *   call before any stream capture begins.
  *   Memory: the array is reserved on every device that loads the library's
  *   module, whether or not this entry point is called.
  *   Concurrency: calls on the same device share the array; two calls that

@@ -685,9 +685,9 @@ kvq_status kvq_selftest_bounded_wait(int32_t* dev_status, void* stream) {
 // cudaMalloc's implicit device-wide synchronization between steps, or a plain C
 // embedding that links only this library and has no device allocator of its
 // own.  This entry point allocates and frees nothing: it looks up the address
-// of the array once per device and passes it down.
+// of the array once per context and passes it down.
 //
-// The array is one per device and shared by all callers of this entry point:
+// The array is one per context of a device and shared by all callers of this entry point:
 // two of its calls that overlap on a device (different streams, or threads
 // without ordering between their streams) race on it and corrupt each other's
 // partial results.  Order them on one stream, or with events.
@@ -700,28 +700,14 @@ namespace {
 
 static __device__ __align__(256) unsigned char g_decode_scratch[KVQ_DECODE_STATIC_SCRATCH_BYTES];
 
-constexpr int kMaxScratchDevices = 64;
-std::mutex g_scratch_mutex;
-void* g_scratch_ptr[kMaxScratchDevices] = {};
+kvq::PerContext<void*> g_scratch;
 
-// Device address of the current device's copy of the scratch; the first call
-// per device looks it up (cudaGetSymbolAddress, with that device current).
-kvq_status scratch_for_current_device(void** ptr) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_status(e, "querying the current device");
-  if (dev < 0 || dev >= kMaxScratchDevices)
-    return fail(KVQ_ERR_UNSUPPORTED, "device %d: the static decode scratch covers devices 0..%d", dev,
-                kMaxScratchDevices - 1);
-  std::lock_guard<std::mutex> lock(g_scratch_mutex);
-  if (g_scratch_ptr[dev] == nullptr) {
-    void* p = nullptr;
-    e = cudaGetSymbolAddress(&p, g_decode_scratch);
-    if (e != cudaSuccess) return cuda_status(e, "looking up the static decode scratch");
-    if (p == nullptr) return fail(KVQ_ERR_CUDA, "the static decode scratch has no device address");
-    g_scratch_ptr[dev] = p;
-  }
-  *ptr = g_scratch_ptr[dev];
+// Device address of the current context's copy of the scratch; the first call
+// per context looks it up (cudaGetSymbolAddress, with that context current).
+kvq_status scratch_for_current_context(void** ptr) {
+  const cudaError_t e = g_scratch.get(ptr, [](void** p) { return cudaGetSymbolAddress(p, g_decode_scratch); });
+  if (e != cudaSuccess) return cuda_status(e, "looking up the static decode scratch");
+  if (*ptr == nullptr) return fail(KVQ_ERR_CUDA, "the static decode scratch has no device address");
   return KVQ_OK;
 }
 
@@ -744,7 +730,7 @@ extern "C" kvq_status kvq_paged_decode_attention_static_scratch(
                 "pass fewer sequences or a smaller num_splits, or use kvq_paged_decode_attention with a workspace",
                 num_seqs, num_splits, need, static_cast<size_t>(KVQ_DECODE_STATIC_SCRATCH_BYTES));
   void* scratch = nullptr;
-  KVQ_TRY(scratch_for_current_device(&scratch));
+  KVQ_TRY(scratch_for_current_context(&scratch));
   return kvq_paged_decode_attention(cfg, q, out, seq_lens, num_seqs, block_tables, max_blocks_per_seq, num_blocks,
                                     k_pool, v_pool, k_tail, v_tail, softmax_scale, scratch,
                                     KVQ_DECODE_STATIC_SCRATCH_BYTES, num_splits, dev_status, stream);

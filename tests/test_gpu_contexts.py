@@ -72,6 +72,13 @@ def run():
                                           None) == 0, lib.kvq_last_error()
     ok(cu.cuCtxSynchronize())
     res = [down(out, host["q"]), down(step, host["q"][:1]), down(mass, np.zeros(8, np.float32))]
+    # the library's own scratch is this context's
+    assert lib.kvq_paged_decode_attention_static_scratch(
+        ctypes.byref(c), b["q"], step, b["lens"], 1, b["table"], 8, 8, b["pool"], b["pool"], b["kt"], b["vt"],
+        2 * d ** -0.5, 0, status, None) == 0, lib.kvq_last_error()
+    ok(cu.cuCtxSynchronize())
+    res.append(down(step, host["q"][:1]))
+    assert not np.array_equal(res[1], res[3])
     assert down(status, np.zeros(4, np.int32))[0] == 0
     for p in held:
         ok(cu.cuMemFree_v2(p))
