@@ -270,9 +270,9 @@ def paged_decode_attention(cfg: Config, q, out, seq_lens, block_tables, k_pool, 
 
 def decode_mass_workspace_bytes(cfg: Config, num_seqs: int, max_blocks_per_seq: int, num_splits: int = 0) -> int:
     out = _sz(0)
-    _check(load_library().kvq_decode_mass_workspace_bytes(ctypes.byref(cfg.c()), num_seqs, max_blocks_per_seq,
-                                                          num_splits, ctypes.byref(out)),
-           "kvq_decode_mass_workspace_bytes")
+    _check(load_library().kvq_decode_mass_workspace_bytes(
+        ctypes.byref(cfg.c()), _int(num_seqs, "num_seqs"), _int(max_blocks_per_seq, "max_blocks_per_seq"),
+        _int(num_splits, "num_splits"), ctypes.byref(out)), "kvq_decode_mass_workspace_bytes")
     return out.value
 
 
@@ -284,7 +284,8 @@ def paged_decode_attention_mass(cfg: Config, q, out, mass, seq_lens, block_table
     CUDA tensor of at least ``decode_mass_workspace_bytes`` bytes."""
     if softmax_scale is None:
         softmax_scale = cfg.head_dim ** -0.5
-    nb = k_pool.shape[0] if num_blocks is None else num_blocks
+    nb = _int(k_pool.shape[0] if num_blocks is None else num_blocks, "num_blocks")
+    splits = _int(num_splits, "num_splits")
     b = seq_lens.shape[0]
     if mass.dim() != 2 or mass.shape[0] != b:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
@@ -300,15 +301,16 @@ def paged_decode_attention_mass(cfg: Config, q, out, mass, seq_lens, block_table
         _ptr(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1])), block_tables.shape[1], nb,
         _ptr(k_pool, "k_pool", torch.uint8), _ptr(v_pool, "v_pool", torch.uint8),
         _ptr(k_tail, "k_tail", torch.float16, tail), _ptr(v_tail, "v_tail", torch.float16, tail), float(softmax_scale),
-        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), num_splits,
+        _ptr(workspace, "workspace", torch.uint8), workspace.numel(), splits,
         _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
     _check(st, "kvq_paged_decode_attention_mass")
 
 
 def evict_workspace_bytes(cfg: Config, num_seqs: int, max_blocks_per_seq: int) -> int:
     out = _sz(0)
-    _check(load_library().kvq_evict_workspace_bytes(ctypes.byref(cfg.c()), num_seqs, max_blocks_per_seq,
-                                                    ctypes.byref(out)), "kvq_evict_workspace_bytes")
+    _check(load_library().kvq_evict_workspace_bytes(
+        ctypes.byref(cfg.c()), _int(num_seqs, "num_seqs"), _int(max_blocks_per_seq, "max_blocks_per_seq"),
+        ctypes.byref(out)), "kvq_evict_workspace_bytes")
     return out.value
 
 
@@ -321,12 +323,13 @@ def evict_tiles(cfg: Config, mass, seq_lens, block_tables, keep_tiles: int, sink
     gets the kept tiles' old indices.  ``workspace``: uint8, at least
     ``evict_workspace_bytes`` bytes."""
     b = seq_lens.shape[0]
+    keep, sink, recent = (_int(keep_tiles, "keep_tiles"), _int(sink_tiles, "sink_tiles"),
+                          _int(recent_tiles, "recent_tiles"))
     if mass.dim() != 2 or mass.shape[0] != b:
         raise ValueError(f"mass has shape {tuple(mass.shape)}, expected ({b}, max_tiles)")
     _on_current_device(mass, seq_lens, block_tables, kept, workspace, dev_status)
     st = load_library().kvq_evict_tiles(
-        ctypes.byref(cfg.c()), _ptr(mass, "mass", torch.float32), mass.shape[1],
-        _int(keep_tiles, "keep_tiles"), _int(sink_tiles, "sink_tiles"), _int(recent_tiles, "recent_tiles"),
+        ctypes.byref(cfg.c()), _ptr(mass, "mass", torch.float32), mass.shape[1], keep, sink, recent,
         _ptr(seq_lens, "seq_lens", torch.int32), b,
         _ptr(block_tables, "block_tables", torch.int32, (b, block_tables.shape[1])), block_tables.shape[1],
         _ptr(kept, "kept", torch.int32, tuple(mass.shape)), _ptr(workspace, "workspace", torch.uint8),
@@ -436,8 +439,10 @@ def _rows(t, name, rows, heads, d):
 def prompt_workspace_bytes(cfg: Config, num_seqs: int, total_tokens: int, max_seq_tokens: int,
                            mass_window: int = 0) -> int:
     out = _sz(0)
-    _check(load_library().kvq_prompt_workspace_bytes(ctypes.byref(cfg.c()), num_seqs, total_tokens, max_seq_tokens,
-                                                     mass_window, ctypes.byref(out)), "kvq_prompt_workspace_bytes")
+    _check(load_library().kvq_prompt_workspace_bytes(
+        ctypes.byref(cfg.c()), _int(num_seqs, "num_seqs"), _int(total_tokens, "total_tokens"),
+        _int(max_seq_tokens, "max_seq_tokens"), _int(mass_window, "mass_window"), ctypes.byref(out)),
+        "kvq_prompt_workspace_bytes")
     return out.value
 
 
@@ -454,6 +459,7 @@ def prompt_attention(cfg: Config, q, k, v, out, cu_seqlens, max_seq_tokens: int,
     if softmax_scale is None:
         softmax_scale = cfg.head_dim ** -0.5
     n, b = q.shape[0], cu_seqlens.shape[0] - 1
+    longest, window = _int(max_seq_tokens, "max_seq_tokens"), _int(mass_window, "mass_window")
     qp, qs = _rows(q, "q", n, cfg.num_q_heads, cfg.head_dim)
     kp, ks = _rows(k, "k", n, cfg.num_kv_heads, cfg.head_dim)
     vp, vs = _rows(v, "v", n, cfg.num_kv_heads, cfg.head_dim)
@@ -464,8 +470,7 @@ def prompt_attention(cfg: Config, q, k, v, out, cu_seqlens, max_seq_tokens: int,
         ctypes.byref(cfg.c()), qp, qs, kp, ks, vp, vs,
         _ptr(out, "out", torch.float16, (n, cfg.num_q_heads, cfg.head_dim)),
         _ptr(lse, "lse", torch.float32, (n, cfg.num_q_heads)), _ptr(cu_seqlens, "cu_seqlens", torch.int32), b, n,
-        _int(max_seq_tokens, "max_seq_tokens"), float(softmax_scale), _ptr(mass, "mass", torch.float32),
-        0 if mass is None else mass.shape[1], _int(mass_window, "mass_window"),
+        longest, float(softmax_scale), _ptr(mass, "mass", torch.float32), 0 if mass is None else mass.shape[1], window,
         _ptr(workspace, "workspace", torch.uint8), 0 if workspace is None else workspace.numel(),
         _ptr(dev_status, "dev_status", torch.int32), _stream(stream))
     _check(st, "kvq_prompt_attention")
