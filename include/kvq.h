@@ -460,10 +460,12 @@ KVQ_API kvq_status kvq_prompt_workspace_bytes(const kvq_config* cfg, int num_seq
  *                  grows with total_tokens x max_seq_tokens (1.0 GB for
  *                  131072 tokens, 8 KV heads, g = 8, T = 64), with a window
  *                  with max_seq_tokens.
- * A row that sees a NaN, or an infinite score, gives NaN, one that sees an
- * infinite value gives infinity or NaN there.  Scores (q.k * softmax_scale) of
- * 1.16e7 (2^24 log2 units) and more in magnitude, whose fp32 numbers have no
- * fraction left, count as infinite of their sign.  Values that a row does not see
+ * A row that sees a NaN or a score of +infinity gives NaN, and NaN to the
+ * masses of the tiles it sees if it counts.  A score of -infinity has no weight;
+ * a row that sees no other gives NaN as well.  A row that sees an infinite value
+ * gives infinity or NaN there.  Scores (q.k * softmax_scale) of 1.16e7 (2^24 log2
+ * units) and more in magnitude, whose fp32 numbers have no fraction left, count
+ * as infinite of their sign.  Values that a row does not see
  * (later tokens, other sequences, rows behind the last one) never reach it,
  * whatever they are.  A sequence whose prefix sums are negative, past
  * total_tokens or longer than max_seq_tokens is skipped, and where they descend

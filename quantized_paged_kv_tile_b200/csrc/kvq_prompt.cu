@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(Geom<D, MASS>::kThreads, 1) prompt_kernel(cons
           for (int k = 0; k < 4; ++k) mx[k] = max3nan(mx[k], s[e - 4 + k], s[e - 4 + k]);
           // (rounded as it is kept, not again inside a multiply-add)
           const float t = __fmul_rn(max3nan(mx[0], mx[1], max3nan(mx[2], mx[3], mx[3])), pd.qscale);
-          if (!(t < kFar)) l = NAN;  // a NaN or an infinite score: the row is NaN
+          if (!(t < kFar)) l = NAN;  // a NaN or a score of +inf: the row is NaN (-inf has no weight)
           return t;
         };
         // The maximum moves to `top` in the lanes where it is more than kLazy

@@ -198,3 +198,11 @@ def test_sequences_from_a_descent_on_are_skipped(before):
             assert bool((mass[:, want_mass.shape[1]:] == 0).all())
     out = call(cfg, q, k, v, [n], 0, cu=[n, 0, n], max_len=n)[0]  # nothing before the descent
     assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_score_of_minus_infinity_has_no_weight(d):
+    cfg, q, k, v, want = hidden_keys(d, 2.0, -math.inf)
+    k[250, 0, 0] = math.inf  # +inf: every row that sees it is NaN
+    out = call(cfg, q, k, v, [300])[0]
+    assert bool(torch.isnan(out[250:]).all()) and torch.equal(out[5:250], want[5:250])
