@@ -206,3 +206,27 @@ def test_a_score_of_minus_infinity_has_no_weight(d):
     k[250, 0, 0] = math.inf  # +inf: every row that sees it is NaN
     out = call(cfg, q, k, v, [300])[0]
     assert bool(torch.isnan(out[250:]).all()) and torch.equal(out[5:250], want[5:250])
+
+
+# ------------------------------------------------------------------ the largest values
+@pytest.mark.parametrize("n,hkv", [(150, 1), (700, 40)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_finite_values_give_finite_rows(d, n, hkv):
+    """A mean of values up to fp16's largest stays in its range, however the
+    weights are rounded (a weight may be up to 2^15 relative to the running
+    maximum, and rounded by 2^-11 of it)."""
+    cfg = config(hkv, 3, d)
+    q, k, v = rows(cfg, n, 41, std=6.0)
+    v.fill_(65504.0)
+    v[:, :, 1::2] = -65504.0
+    out, _, _, status = call(cfg, q, k, v, [n])
+    assert status == 0
+    want = v[:1].double().repeat_interleave(3, 1)
+    assert bool(((out.double() - want).abs() <= (2 * U16 + n * U32) * 65504.0).all())
+    # an infinite value is still infinite, from its token on
+    v[70, :, 6] = math.inf
+    v[90, :, 9] = -math.inf
+    out, _, _, _ = call(cfg, q, k, v, [n])
+    assert bool((out[70:, :, 6] == math.inf).logical_or(out[70:, :, 6].isnan()).all())
+    assert bool((out[90:, :, 9] == -math.inf).logical_or(out[90:, :, 9].isnan()).all())
+    assert bool(torch.isfinite(out[:70]).all())
