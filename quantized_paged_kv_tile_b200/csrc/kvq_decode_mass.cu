@@ -7,7 +7,10 @@
 // with l_t,h the sum of tile t's weights relative to the running maximum
 // m_t,h it had, and M_h, L_h the head's final maximum and sum.  The statistics
 // are 8 bytes per (tile, query head) against the tile's 9216 bytes per KV head
-// (T = 64, 4-bit codes).
+// (T = 64, 4-bit codes).  6 sequences of 131073 tokens, 8 x 4 heads: 310 us in a
+// graph against 285 without masses.  21 of the 25 are in the tile kernel (a second
+// running sum, two shuffles and a store a tile, in code that is bound by issue
+// slots), 4 in the pass below.
 #include "kvq_decode_kernel.cuh"
 #include "kvq_launch.cuh"
 

@@ -33,10 +33,12 @@
 // a thread take two warps of a scheduler that long) and takes about 3300, the
 // chain P -> P V -> Q K^T -> S -> maximum -> exponentials of a query tile; long
 // calls run into the power limit first (1567 MHz at 1000 W; a library fp16
-// GEMM of 8192^3 settles at 1287 TFLOP/s there, this kernel at 1050: 16384
-// tokens x 64 heads in 4.16 to 4.27 ms, 1218 TFLOP/s in short runs).  Replacing 1/8 to
-// 3/8 of the exponentials by a polynomial on the FMA pipe gained 1.6% on short
-// runs and lost 4 to 11% on long ones.
+// GEMM of 8192^3 settles at 1287 TFLOP/s there, this kernel at 1030 to 1100).
+// 16384 tokens x 64 heads: K channels of one std 3.44 ms in five calls (1279
+// TFLOP/s) and 4.01 in 400; of very different stds, whose scores move the
+// maximum further, 3.76 and 4.29.  Replacing 1/8 to 3/8 of the exponentials by a
+// polynomial on the FMA pipe gained 1.6% on short runs and lost 4 to 11% on long
+// ones.
 //
 // What a mask hides never reaches a result: masked scores become -inf by
 // selection; V rows past the sequence are zeroed in shared memory; V values
@@ -47,8 +49,8 @@
 // maximum it is relative to, goes to a scratch area of the CTA; once a query
 // tile's l and m are final, the rows that count are weighted and summed, and a
 // second kernel adds the query tiles of a sequence to its masses in a fixed
-// order.  It costs a fifth of the attention (4096 tokens x 128 heads: 544 us
-// without, 656 with all queries counting).
+// order.  It costs a sixth of the attention (4 x 4096 tokens, 32 heads: 542 us
+// without, 626 with all queries counting).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -1223,13 +1225,12 @@ PromptSizes prompt_sizes(const kvq_config& cfg, int num_seqs, int total_tokens, 
   z.units = prompt_units(cfg, num_seqs, total_tokens);
   // With no more units than SMs a call takes as long as its longest unit: then
   // a unit is one query tile and the CTA's two streams take half of its keys
-  // each.  Pairs of query tiles against halves of the keys, us (d, heads,
-  // tokens), up to 148 units of pairs: 128, 2 over 1, 1024: 27 / 21; 3093: 53 /
-  // 38; 128, 8 over 1, 4736 (148 units): 95 / 72; 128, 16 over 2, 2368 (148):
-  // 60 / 50; 64, 4 over 1, 6400: 94 / 57; and beyond, where CTAs take several
-  // units and a pair loads each key tile once for two: 128, 16 over 2, 3000
-  // (188): 72 / 71; 4096 (256): 80 / 95; 8192: 239 / 277; 64, 16 over 2, 4096
-  // (256): 71 / 76.
+  // each.  Pairs of query tiles against halves of the keys, us in a graph, d =
+  // 128 / d = 64: 34 units of pairs (1024 tokens, 8 heads over 2) 21.5 against
+  // 16.1 / 20.1 against 14.3; 148 (3050, 12 over 4) 49.5, 37.7 / 44.7, 32.1, with
+  // masses 59.7, 47.4 / 56.7, 41.6.  Beyond, CTAs take several units and a pair
+  // loads each key tile once for two: 192 (4000, 12 over 4) 64.3, 63.6 / 57.2,
+  // 52.1; 256 (4096, 16 over 2) 80, 95 / 71, 76.
   z.split = query_tiles(cfg) == 2 && z.units <= sms;
   if (z.split) z.units = (static_cast<long long>(total_tokens) / W1 + num_seqs) * cfg.num_kv_heads;
   z.max_tiles_k = (max_seq_tokens + keys - 1) / keys;
